@@ -12,28 +12,14 @@
 // The transposed products use the GEMM's transposed-operand modes (A stored [K][M], B stored
 // [N][K]), so no transposed copy of any tensor is made. The final sum over shards runs in the fused
 // ring GEMM when the token count allows it.
-#include <cuda_bf16.h>
-
 #include <cstring>
 
+#include "act.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
 namespace tpx {
 namespace {
-
-__device__ __forceinline__ float gelu_grad(float x) {
-  // d/dx [x Phi(x)] = Phi(x) + x phi(x)
-  return 0.5f * (1.0f + erff(x * 0.70710678118654752f)) + x * 0.39894228040143268f * __expf(-0.5f * x * x);
-}
-__device__ __forceinline__ float gelu_tanh_grad(float x) {
-  const float c = 0.79788456080286536f, a = 0.044715f;
-  const float th = tanhf(c * (x + a * x * x * x));
-  return 0.5f * (1.0f + th) + 0.5f * x * (1.0f - th * th) * c * (1.0f + 3.0f * a * x * x);
-}
-
-__device__ __forceinline__ float bf(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-__device__ __forceinline__ uint16_t to_bf(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
 // rows = t*N stacked rows; f = columns of dZ. H and dH have wn = f (GeLU) or 2f (SwiGLU) columns.
 // VEC consecutive columns per step.
