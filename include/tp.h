@@ -320,6 +320,133 @@ tp_status tp_layer_fwd(const uint16_t* x, const uint16_t* const* o, int64_t N, i
                        uint16_t* h1_bf16, uint16_t* z_ws, float* const* partials, float* const* y, void* stream);
 
 /* ------------------------------------------------------------------------------------------------
+ * Mixture-of-experts MLP. The pages name expert parallelism without an operator ([CH05] §5.3 AllToAll);
+ * the formulas are in each comment. N tokens, E experts, k choices for a token, R = N*k rows at most.
+ *
+ * Rows sorted by expert. A router's choice gives each (token, choice) one row. Rows are sorted by
+ * expert, tokens ascending inside an expert: `offsets` int32 [E + 1] (expert e holds rows offsets[e] ..
+ * offsets[e+1] - 1; offsets[E] <= R rows in all), `row_token` int32 [R] (the token of a row),
+ * `slot` int32 [N, k] (the row of a choice, -1 for none). These live on the device and the host never
+ * reads them, so a step needs no synchronisation and can be captured in a graph.
+ *
+ * Ragged products take any such segments:
+ *   - offsets are taken as clamped to 0..R, a segment that ends before it begins as empty. Segments
+ *     must not overlap. Rows of the output that belong to no segment (those behind the last, above all)
+ *     are left as they were; rows of the input that belong to none are not read into any result.
+ *   - E is 1..TP_MAX_EXPERTS (TP_EUNSUPPORTED above). k and n multiples of 8, pointers aligned; all
+ *     matrices are contiguous.
+ *   - Sums are binary32 on the tensor cores, whose adds truncate: relative error about
+ *     (contraction / 32) * 2^-24 before the one rounding to the output type.
+ *   - Results do not depend on launch shape or timing (no atomics), and no call keeps state.
+ * ------------------------------------------------------------------------------------------------ */
+#define TP_MAX_EXPERTS 1024
+#define TP_MAX_TOPK 16
+
+/* How a choice's weight follows from the logits l: SOFTMAX takes softmax over all experts, TOPK the
+ * softmax over the chosen ones (the k weights of a token then sum to 1). */
+typedef enum { TP_GATE_SOFTMAX = 0, TP_GATE_TOPK = 1 } tp_gate;
+
+/* Router: for every token the k experts of the largest logits, in descending order, ties to the lowest
+ * index; weight fp32 [N, k] as `gate` says; and the rows sorted by expert. An expert whose logit is
+ * -inf (or NaN) is masked: it is never chosen. A token with fewer than k experts left gets expert -1,
+ * weight 0 and slot -1 in the remaining choices, and no rows for them; a token with all masked gets
+ * none. +inf counts as the largest finite number. row_token behind offsets[E] is left as it was.
+ * logits [N, E] fp32 or bf16, pointers aligned to their elements; k <= E, k <= TP_MAX_TOPK.
+ * The workspace is tp_moe_route_ws_bytes (0 for N <= 64: ws may be NULL). N = 0 writes nothing. */
+size_t tp_moe_route_ws_bytes(int64_t N, int E, int k);
+tp_status tp_moe_route(const void* logits, tp_dtype dtype, int64_t N, int E, int k, tp_gate gate, int32_t* expert,
+                       float* weight, int32_t* slot, int32_t* offsets, int32_t* row_token, void* ws, size_t ws_bytes,
+                       void* stream);
+/* Gradient of the logits ([N, E], dtype of the logits) from dweight fp32 [N, k]. With q the softmax that
+ * `gate` names: dl_i = q_i (dw_i - sum_j q_j dw_j), dw_i = 0 for experts that were not chosen (for
+ * TOPK, q_i = 0 there too). dweight of a choice that is -1 is not used. The choice itself (and the
+ * order of ties) has no gradient. */
+tp_status tp_moe_route_bwd(const void* logits, tp_dtype dtype, int64_t N, int E, int k, tp_gate gate, const int32_t* expert,
+                           const float* dweight, void* dlogits, void* stream);
+
+/* Product grouped by expert: y[i] = act(x[row_index[i]] . w[e]) for every row i of every expert e.
+ *   x          bf16 [x_rows, k]; row_index int32 [R] (NULL: row i of x itself, x_rows >= R). An index
+ *              outside 0..x_rows-1 reads as a row of zeros; an index may repeat.
+ *   w          bf16 [E, k, n] ([E, k, 2n] = [gate | up] for SWIGLU)
+ *   y          [R, n], y_dtype fp32 or bf16
+ *   pre        optional bf16 output, what act is applied to: [R, n] ([R, 2n] for SWIGLU); NULL for
+ *              TP_ACT_NONE. The backward pass reads it as h_pre.
+ * One token's few rows (decode) and a prompt's thousands take the same call. */
+tp_status tp_ragged_linear(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const int32_t* offsets, int64_t R,
+                           int E, int64_t k, int64_t n, tp_act act, const uint16_t* w, void* y, tp_dtype y_dtype,
+                           uint16_t* pre, void* stream);
+/* Its input gradient, through the activation that made its input: with dy bf16 [R, n], w bf16 [E, k, n] and
+ * dz[i] = dy[i] . w[e]^T ([R, k], binary32, not rounded),
+ *   TP_ACT_NONE  dx = dz, bf16 [R, k], h_pre NULL
+ *   GELU*        dx = act'(h_pre) * dz, h_pre bf16 [R, k]
+ *   SWIGLU       dx = [dz * up * silu'(gate) | dz * silu(gate)], bf16 [R, 2k], h_pre = [gate | up] [R, 2k] */
+tp_status tp_ragged_linear_dx(const uint16_t* dy, const int32_t* offsets, int64_t R, int E, int64_t k, int64_t n,
+                              const uint16_t* w, tp_act act, const uint16_t* h_pre, uint16_t* dx, void* stream);
+/* Its weight gradient: dw[e] = sum over e's rows i of x[row_index[i]]^T dy[i]; dw [E, k, n], fp32 or bf16
+ * (rounded once). An expert without rows gets zeros, also when R = 0. Spans of 512 rows are summed in
+ * binary32 round-to-nearest, in row order. x, row_index as in tp_ragged_linear, dy bf16 [R, n]. */
+tp_status tp_ragged_linear_dw(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const uint16_t* dy,
+                              const int32_t* offsets, int64_t R, int E, int64_t k, int64_t n, void* dw, tp_dtype dw_dtype,
+                              void* stream);
+
+/* Combine: y[n] = sum_j weight[n, j] * u[slot[n, j]], j ascending, binary32, rounded once. u [R, h] and
+ * y [N, h] fp32 or bf16; weight NULL means ones; a slot outside 0..R-1 adds nothing. h a multiple of 8,
+ * aligned. */
+tp_status tp_moe_combine(const void* u, tp_dtype u_dtype, int64_t R, const float* weight, const int32_t* slot, int64_t N,
+                         int64_t h, int k, void* y, tp_dtype y_dtype, void* stream);
+/* Its gradients: du[slot[n, j]] = weight[n, j] * dy[n] (bf16 [R, h]; rows that no slot names are left as
+ * they were; no two slots may name the same row) and dweight[n, j] = <dy[n], u[slot[n, j]]> (fp32 [N, k],
+ * 0 for a slot outside 0..R-1). */
+tp_status tp_moe_combine_bwd(const void* dy, tp_dtype dy_dtype, const void* u, tp_dtype u_dtype, int64_t R,
+                             const float* weight, const int32_t* slot, int64_t N, int64_t h, int k, uint16_t* du,
+                             float* dweight, void* stream);
+
+/* The whole MLP: route, z = act(x[row_token] . w_in[e]), u = z . w_down[e], y = combine(u).
+ *   x bf16 [N, h]; logits [N, E]; w_in bf16 [E, h, F] ([E, h, 2F] for SWIGLU); w_down bf16 [E, F, h]
+ *   expert, weight, slot, offsets, row_token: outputs as of tp_moe_route, kept for the backward pass
+ *   h_pre  bf16 [R, F] ([R, 2F]), optional: kept for the backward pass;  z bf16 [R, F];  u bf16 [R, h]
+ *   y      [N, h] fp32 or bf16
+ * Four products' worth of launches on one stream, nothing read back. Workspace tp_moe_mlp_ws_bytes. */
+size_t tp_moe_mlp_ws_bytes(int64_t N, int E, int k);
+tp_status tp_moe_mlp_fwd(const uint16_t* x, int64_t N, int64_t h, int64_t F, int E, int k, tp_gate gate, tp_act act,
+                         const void* logits, tp_dtype logits_dtype, const uint16_t* w_in, const uint16_t* w_down,
+                         int32_t* expert, float* weight, int32_t* slot, int32_t* offsets, int32_t* row_token,
+                         uint16_t* h_pre, uint16_t* z, uint16_t* u, void* y, tp_dtype y_dtype, void* ws, size_t ws_bytes,
+                         void* stream);
+/* Its gradients from dy bf16 [N, h] and what the forward pass kept. Scratch: du_ws bf16 [R, h], dh_ws bf16
+ * [R, F] ([R, 2F] for SWIGLU), dweight_ws fp32 [N, k]. Outputs: dw_in and dw_down fp32 in their weights'
+ * shapes, dx [N, h] fp32 or bf16, dlogits [N, E] in the logits' type. N = 0 clears dw_in and dw_down. */
+tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64_t h, int64_t F, int E, int k, tp_gate gate,
+                         tp_act act, const void* logits, tp_dtype logits_dtype, const uint16_t* w_in,
+                         const uint16_t* w_down, const int32_t* expert, const float* weight, const int32_t* slot,
+                         const int32_t* offsets, const int32_t* row_token, const uint16_t* h_pre, const uint16_t* z,
+                         const uint16_t* u, uint16_t* du_ws, uint16_t* dh_ws, float* dweight_ws, float* dw_in,
+                         float* dw_down, void* dx, tp_dtype dx_dtype, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Low-rank adapters of many requests at once beside a column-parallel projection (serving): for every
+ * token i with adapter a = id[i],   y[r][i] = x[i] . w[r] + scale[a] * (x[i] . A[a]) . B[r][a],
+ * the shared projection and the adapters' part accumulated together in binary32 and rounded once;
+ * x . A is held in binary32 in between and enters the second product to 16 bits of mantissa.
+ * ------------------------------------------------------------------------------------------------ */
+/* Plan of a batch, made once and used by every projection of every layer: the tokens sorted by adapter.
+ * id int32 [N]; an id outside 0..L-1 (say -1) means no adapter. offsets int32 [L + 1]; row_token int32
+ * [N]: every token once, adapter ascending, tokens ascending inside one, those without an adapter last
+ * (from offsets[L] on). L is 1..TP_MAX_EXPERTS. Workspace tp_lora_plan_ws_bytes (0 for N <= 64). */
+size_t tp_lora_plan_ws_bytes(int64_t N, int L);
+tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, int32_t* row_token, void* ws, size_t ws_bytes,
+                       void* stream);
+/* x bf16 [N, k]; w bf16 stacked [t, k, n/t] as in tp_column_linear; A bf16 [L, k, rank]; B bf16
+ * [t, L, rank, n/t]; scale fp32 [L] or NULL (ones); y bf16 stacked [t, N, n/t]. row_token must name every
+ * token once (a token that it does not name keeps its rows of y; an index outside 0..N-1 is skipped).
+ * Adapters of a smaller rank are padded with zeros in A's columns or B's rows. k, n/t and rank multiples
+ * of 8, aligned. Workspace tp_lora_ws_bytes = N * rank fp32. */
+size_t tp_lora_ws_bytes(int64_t N, int rank);
+tp_status tp_lora_linear(const uint16_t* x, int64_t N, int64_t k, int64_t n, int t, const uint16_t* w, int L, int rank,
+                         const uint16_t* a, const uint16_t* b, const float* scale, const int32_t* offsets,
+                         const int32_t* row_token, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
  * tp_mlp_fwd without caller-provided scratch. The pages have no counterpart: this entry point exists
  * for callers that cannot allocate device memory. Examples are code inside a host framework whose
  * caching pool owns the GPU's memory, where an allocation behind the pool's back can fail or escape

@@ -30,6 +30,8 @@ TP_CASE2_ALLGATHER, TP_CASE2_ALLREDUCE = 0, 1
 TP_CASE3_ALLREDUCE, TP_CASE3_RS_B, TP_CASE3_RS_F = 0, 1, 2
 TP_CASE4_GATHER_X, TP_CASE4_GATHER_W = 0, 1
 TP_MAX_SHARDS = 16
+TP_GATE_SOFTMAX, TP_GATE_TOPK = 0, 1
+TP_MAX_EXPERTS, TP_MAX_TOPK = 1024, 16
 
 EXPORTED = (
     "tp_status_str", "tp_last_error", "tp_device_status", "tp_set_wait_budget", "tp_selftest_wait_timeout",
@@ -37,6 +39,9 @@ EXPORTED = (
     "tp_all_gather", "tp_all_reduce", "tp_grouped_gemm", "tp_column_linear", "tp_row_linear", "tp_row_linear_reduce", "tp_mlp_fwd",
     "tp_sharded_matmul_ws_bytes", "tp_sharded_matmul_choose", "tp_sharded_matmul", "tp_layer_fwd", "tp_mlp_fwd_noalloc",
     "tp_column_linear_sp", "tp_mlp_fwd_sp", "tp_all_to_all", "tp_grouped_gemm_t", "tp_mlp_bwd",
+    "tp_moe_route_ws_bytes", "tp_moe_route", "tp_moe_route_bwd", "tp_ragged_linear", "tp_ragged_linear_dx",
+    "tp_ragged_linear_dw", "tp_moe_combine", "tp_moe_combine_bwd", "tp_moe_mlp_ws_bytes", "tp_moe_mlp_fwd",
+    "tp_moe_mlp_bwd", "tp_lora_plan_ws_bytes", "tp_lora_plan", "tp_lora_ws_bytes", "tp_lora_linear",
 )
 
 _vp, _i64, _i32, _u64, _sz = C.c_void_p, C.c_int64, C.c_int, C.c_uint64, C.c_size_t
@@ -72,6 +77,21 @@ _SIGS = {
     "tp_sharded_matmul": (_i32, [_i32, _i32, _pp, _pp, _i64, _i64, _i64, _i32, _pp, _i32, _vp, _sz, _vp]),
     "tp_layer_fwd": (_i32, [_vp, _pp, _i64, _i64, _i32, _i32, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _pp,
                             _vp, _vp, _pp, _pp, _vp]),
+    "tp_moe_route_ws_bytes": (_sz, [_i64, _i32, _i32]),
+    "tp_moe_route": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "tp_moe_route_bwd": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "tp_ragged_linear": (_i32, [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp]),
+    "tp_ragged_linear_dx": (_i32, [_vp, _vp, _i64, _i32, _i64, _i64, _vp, _i32, _vp, _vp, _vp]),
+    "tp_ragged_linear_dw": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _vp, _i32, _vp]),
+    "tp_moe_combine": (_i32, [_vp, _i32, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _i32, _vp]),
+    "tp_moe_combine_bwd": (_i32, [_vp, _i32, _vp, _i32, _i64, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "tp_moe_mlp_ws_bytes": (_sz, [_i64, _i32, _i32]),
+    "tp_moe_mlp_fwd": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32] + [_vp] * 11 + [_i32, _vp, _sz, _vp]),
+    "tp_moe_mlp_bwd": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _i32, _i32, _vp, _i32] + [_vp] * 16 + [_i32, _vp, _vp]),
+    "tp_lora_plan_ws_bytes": (_sz, [_i64, _i32]),
+    "tp_lora_plan": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "tp_lora_ws_bytes": (_sz, [_i64, _i32]),
+    "tp_lora_linear": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _i32] + [_vp] * 7 + [_sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -253,3 +273,77 @@ def tp_layer_fwd(x, o, N, h, n_h, n_kv, d_h, F, t, w_qkv, w_o, w_gu, w_down, qkv
     _call("tp_layer_fwd", _ptr(x), _ptrs(o), N, h, n_h, n_kv, d_h, F, t, _ptr(w_qkv), _ptr(w_o), _ptr(w_gu),
           _ptr(w_down), _ptr(qkv_out), _ptrs(h1), _ptr(h1_bf16), _ptr(z_ws), _ptrs(partials), _ptrs(y),
           _stream(stream))
+
+
+# ---- mixture-of-experts MLP and adapters --------------------------------------------------------
+def tp_moe_route_ws_bytes(N, E, k) -> int:
+    return int(_lib.tp_moe_route_ws_bytes(N, E, k))
+
+
+def tp_moe_route(logits, dtype, N, E, k, gate, expert, weight, slot, offsets, row_token, ws, ws_bytes, stream=None):
+    _call("tp_moe_route", _ptr(logits), dtype, N, E, k, gate, _ptr(expert), _ptr(weight), _ptr(slot), _ptr(offsets),
+          _ptr(row_token), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def tp_moe_route_bwd(logits, dtype, N, E, k, gate, expert, dweight, dlogits, stream=None):
+    _call("tp_moe_route_bwd", _ptr(logits), dtype, N, E, k, gate, _ptr(expert), _ptr(dweight), _ptr(dlogits),
+          _stream(stream))
+
+
+def tp_ragged_linear(x, x_rows, row_index, offsets, R, E, k, n, act, w, y, y_dtype, pre=None, stream=None):
+    _call("tp_ragged_linear", _ptr(x), x_rows, _ptr(row_index), _ptr(offsets), R, E, k, n, act, _ptr(w), _ptr(y), y_dtype,
+          _ptr(pre), _stream(stream))
+
+
+def tp_ragged_linear_dx(dy, offsets, R, E, k, n, w, act, h_pre, dx, stream=None):
+    _call("tp_ragged_linear_dx", _ptr(dy), _ptr(offsets), R, E, k, n, _ptr(w), act, _ptr(h_pre), _ptr(dx), _stream(stream))
+
+
+def tp_ragged_linear_dw(x, x_rows, row_index, dy, offsets, R, E, k, n, dw, dw_dtype, stream=None):
+    _call("tp_ragged_linear_dw", _ptr(x), x_rows, _ptr(row_index), _ptr(dy), _ptr(offsets), R, E, k, n, _ptr(dw), dw_dtype,
+          _stream(stream))
+
+
+def tp_moe_combine(u, u_dtype, R, weight, slot, N, h, k, y, y_dtype, stream=None):
+    _call("tp_moe_combine", _ptr(u), u_dtype, R, _ptr(weight), _ptr(slot), N, h, k, _ptr(y), y_dtype, _stream(stream))
+
+
+def tp_moe_combine_bwd(dy, dy_dtype, u, u_dtype, R, weight, slot, N, h, k, du, dweight, stream=None):
+    _call("tp_moe_combine_bwd", _ptr(dy), dy_dtype, _ptr(u), u_dtype, R, _ptr(weight), _ptr(slot), N, h, k, _ptr(du),
+          _ptr(dweight), _stream(stream))
+
+
+def tp_moe_mlp_ws_bytes(N, E, k) -> int:
+    return int(_lib.tp_moe_mlp_ws_bytes(N, E, k))
+
+
+def tp_moe_mlp_fwd(x, N, h, F, E, k, gate, act, logits, logits_dtype, w_in, w_down, expert, weight, slot, offsets,
+                   row_token, h_pre, z, u, y, y_dtype, ws, ws_bytes, stream=None):
+    _call("tp_moe_mlp_fwd", _ptr(x), N, h, F, E, k, gate, act, _ptr(logits), logits_dtype, _ptr(w_in), _ptr(w_down),
+          _ptr(expert), _ptr(weight), _ptr(slot), _ptr(offsets), _ptr(row_token), _ptr(h_pre), _ptr(z), _ptr(u), _ptr(y),
+          y_dtype, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def tp_moe_mlp_bwd(x, dy, N, h, F, E, k, gate, act, logits, logits_dtype, w_in, w_down, expert, weight, slot, offsets,
+                   row_token, h_pre, z, u, du_ws, dh_ws, dweight_ws, dw_in, dw_down, dx, dx_dtype, dlogits, stream=None):
+    _call("tp_moe_mlp_bwd", _ptr(x), _ptr(dy), N, h, F, E, k, gate, act, _ptr(logits), logits_dtype, _ptr(w_in),
+          _ptr(w_down), _ptr(expert), _ptr(weight), _ptr(slot), _ptr(offsets), _ptr(row_token), _ptr(h_pre), _ptr(z),
+          _ptr(u), _ptr(du_ws), _ptr(dh_ws), _ptr(dweight_ws), _ptr(dw_in), _ptr(dw_down), _ptr(dx), dx_dtype,
+          _ptr(dlogits), _stream(stream))
+
+
+def tp_lora_plan_ws_bytes(N, L) -> int:
+    return int(_lib.tp_lora_plan_ws_bytes(N, L))
+
+
+def tp_lora_plan(id, N, L, offsets, row_token, ws, ws_bytes, stream=None):
+    _call("tp_lora_plan", _ptr(id), N, L, _ptr(offsets), _ptr(row_token), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def tp_lora_ws_bytes(N, rank) -> int:
+    return int(_lib.tp_lora_ws_bytes(N, rank))
+
+
+def tp_lora_linear(x, N, k, n, t, w, L, rank, a, b, scale, offsets, row_token, y, ws, ws_bytes, stream=None):
+    _call("tp_lora_linear", _ptr(x), N, k, n, t, _ptr(w), L, rank, _ptr(a), _ptr(b), _ptr(scale), _ptr(offsets),
+          _ptr(row_token), _ptr(y), _ptr(ws), ws_bytes, _stream(stream))

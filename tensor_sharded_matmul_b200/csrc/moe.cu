@@ -1,0 +1,756 @@
+// The router of a mixture-of-experts MLP (softmax top-k, rows sorted by expert) and the combine of the
+// experts' rows, with their gradients; and the same sort for adapters.
+//
+// Router: a warp takes one token, its E logits spread over the lanes (lane l holds experts l, l + 32,
+// ...). The largest is found k times with two warp reductions each: the order-preserving integer key,
+// then the lowest index among the lanes that hold it. Everything is binary32.
+//
+// Sort by expert: tokens of a block of 64 set one bit each in a bitmap per expert, so a token's place
+// among its expert's rows of the block is a population count: no atomic's order enters. Per-block
+// counts are scanned per expert (one warp each), and every block places its own tokens. A batch of at
+// most 64 tokens is one block and one launch.
+//
+// Combine: y_n = sum_j weight_nj u[slot_nj], bound by reading u: one thread per eight columns, the k
+// rows' loads issued together. Its gradient reads dy and the k rows once, a warp per token.
+#include <cfloat>
+#include <cstring>
+
+#include "ragged.cuh"
+
+namespace tpx {
+namespace {
+
+constexpr int TB = 64;                // tokens per block of the router and the sort
+constexpr int WORDS = TB / 32;
+constexpr int ROUTE_THREADS = 512;
+
+// Order-preserving integer of a float (no NaN): a < b <=> key(a) < key(b). key(-inf) = 0x007fffff.
+constexpr uint32_t KEY_MASKED = 0x007fffffu;
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);      // -0 orders like +0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* logits, int64_t at) {
+  const float x = BF16 ? bf(__ldg(static_cast<const uint16_t*>(logits) + at)) : __ldg(static_cast<const float*>(logits) + at);
+  // NaN masks like -inf; +inf counts as the largest finite number
+  return x != x ? -INFINITY : fminf(x, FLT_MAX);
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+
+struct SortParams {
+  int64_t N;
+  int E, k;                  // buckets, entries per token
+  int rest;                  // 1: entries outside 0..E-1 form a last bucket (rows behind offsets[E])
+  int blocks;
+  int32_t* expert;           // [N][k]
+  int32_t* slot;             // [N][k] or nullptr
+  int32_t* offsets;          // [E + 1]
+  int32_t* row_token;        // [N * k]
+  int32_t* counts;           // [E + rest][blocks], then the buckets' totals [E + rest]
+};
+
+// Sets the bits of this block's entries; `bits`: [buckets][WORDS], cleared before.
+__device__ __forceinline__ void mark_entries(const SortParams& p, uint32_t* bits, int64_t n0) {
+  for (int i = threadIdx.x; i < TB * p.k; i += blockDim.x) {
+    const int t = i / p.k;
+    if (n0 + t >= p.N) break;
+    int e = p.expert[(n0 + t) * p.k + (i - t * p.k)];
+    if (p.rest && (e < 0 || e >= p.E)) e = p.E;
+    if (e >= 0) atomicOr(bits + e * WORDS + t / 32, 1u << (t % 32));
+  }
+}
+__device__ __forceinline__ void clear_bits(uint32_t* bits, int buckets) {
+  for (int i = threadIdx.x; i < buckets * WORDS; i += blockDim.x) bits[i] = 0u;
+}
+__device__ __forceinline__ int bucket_count(const uint32_t* bits, int e) {
+  int c = 0;
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) c += __popc(bits[e * WORDS + w]);
+  return c;
+}
+
+// Exclusive scan of `n` values in shared memory in place, the total behind them. One warp.
+__device__ __forceinline__ void scan_in_place(int* v, int n, int lane) {
+  int base = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int x = i < n ? v[i] : 0;
+    int inc = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    if (i < n) v[i] = base + inc - x;
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) v[n] = base;
+  __syncwarp();
+}
+
+// Writes slot and row_token of this block's entries. start[e]: the block's first row in bucket e.
+__device__ __forceinline__ void place_entries(const SortParams& p, const uint32_t* bits, const int* start, int64_t n0) {
+  for (int i = threadIdx.x; i < TB * p.k; i += blockDim.x) {
+    const int t = i / p.k;
+    if (n0 + t >= p.N) break;
+    const int64_t at = (n0 + t) * p.k + (i - t * p.k);
+    int e = p.expert[at];
+    if (p.rest && (e < 0 || e >= p.E)) e = p.E;
+    int row = -1;
+    if (e >= 0) {
+      row = start[e] + __popc(bits[e * WORDS + t / 32] & ((1u << (t % 32)) - 1u));
+      for (int w = 0; w < t / 32; ++w) row += __popc(bits[e * WORDS + w]);
+      p.row_token[row] = static_cast<int32_t>(n0 + t);
+    }
+    if (p.slot != nullptr) p.slot[at] = row;
+  }
+}
+
+// One block holds the whole batch: offsets and places from its bitmap alone.
+__device__ __forceinline__ void place_alone(const SortParams& p, const uint32_t* bits, int* start) {
+  const int buckets = p.E + p.rest;
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x) start[e] = bucket_count(bits, e);
+  __syncthreads();
+  if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
+  place_entries(p, bits, start, 0);
+}
+
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const void* __restrict__ logits, int gate,
+                                                              float* __restrict__ weight, SortParams p) {
+  extern __shared__ int s_dyn[];
+  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);         // [E][WORDS]
+  int* start = s_dyn + p.E * WORDS;                            // [E + 1]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
+  clear_bits(bits, p.E);
+  __syncthreads();
+  for (int t = warp; t < TB && n0 + t < p.N; t += ROUTE_THREADS / 32) {
+    const int64_t n = n0 + t;
+    uint32_t key[VPL];
+    float m = -INFINITY;
+    float v[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < p.E ? load_logit<BF16>(logits, n * p.E + e) : -INFINITY;
+      key[i] = key_of(v[i]);
+      m = fmaxf(m, v[i]);
+    }
+    m = warp_max(m);
+    float total = 0.0f;
+    if (gate == TP_GATE_SOFTMAX && m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) total += expf(v[i] - m);
+      total = warp_sum(total);
+    }
+    int my_e = -1;
+    float my_w = 0.0f;                                         // lane j: the j-th choice
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t best = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (key[i] > best) { best = key[i]; at = i; }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+      if (top <= KEY_MASKED) break;                            // no expert left
+      const unsigned e = __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(lane + 32 * at) : 0xffffffffu);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane + 32 * i == static_cast<int>(e)) key[i] = 0;
+      if (lane == j) {
+        my_e = static_cast<int>(e);
+        my_w = expf(of_key(top) - m);
+      }
+    }
+    if (gate == TP_GATE_TOPK) total = warp_sum(my_w);
+    if (lane < p.k) {
+      p.expert[n * p.k + lane] = my_e;
+      weight[n * p.k + lane] = my_e >= 0 ? my_w / total : 0.0f;
+      if (my_e >= 0) atomicOr(bits + my_e * WORDS + t / 32, 1u << (t % 32));
+    }
+  }
+  __syncthreads();
+  if (p.blocks == 1) {
+    place_alone(p, bits, start);
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
+      p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = bucket_count(bits, e);
+  }
+}
+
+__global__ void __launch_bounds__(256) sort_count_kernel(SortParams p) {
+  extern __shared__ int s_dyn[];
+  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);
+  const int buckets = p.E + p.rest;
+  clear_bits(bits, buckets);
+  __syncthreads();
+  mark_entries(p, bits, static_cast<int64_t>(blockIdx.x) * TB);
+  __syncthreads();
+  if (p.blocks == 1) {
+    place_alone(p, bits, s_dyn + buckets * WORDS);
+    return;
+  }
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+    p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = bucket_count(bits, e);
+}
+
+// One warp per bucket: its blocks' counts become the rows before each block; the total goes behind all.
+__global__ void __launch_bounds__(256) sort_scan_kernel(SortParams p) {
+  const int lane = threadIdx.x % 32;
+  const int e = blockIdx.x * 8 + threadIdx.x / 32;
+  const int buckets = p.E + p.rest;
+  if (e >= buckets) return;
+  int32_t* c = p.counts + static_cast<int64_t>(e) * p.blocks;
+  int base = 0;
+  for (int b0 = 0; b0 < p.blocks; b0 += 32) {
+    const int b = b0 + lane;
+    const int x = b < p.blocks ? c[b] : 0;
+    int inc = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    if (b < p.blocks) c[b] = base + inc - x;
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) p.counts[static_cast<int64_t>(buckets) * p.blocks + e] = base;
+}
+
+__global__ void __launch_bounds__(256) sort_place_kernel(SortParams p) {
+  extern __shared__ int s_dyn[];
+  const int buckets = p.E + p.rest;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);
+  int* start = s_dyn + buckets * WORDS;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
+  clear_bits(bits, buckets);
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+    start[e] = p.counts[static_cast<int64_t>(buckets) * p.blocks + e];
+  __syncthreads();
+  mark_entries(p, bits, n0);
+  if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
+  __syncthreads();
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+    start[e] += p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
+  __syncthreads();
+  place_entries(p, bits, start, n0);
+}
+
+// dlogits of one token per warp. With q the weights' softmax (over all experts, or over the chosen):
+// dl_i = q_i (dw_i - sum_j q_j dw_j), dw zero where not chosen.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(256) route_bwd_kernel(const void* __restrict__ logits, int64_t N, int E, int k, int gate,
+                                                        const int32_t* __restrict__ expert,
+                                                        const float* __restrict__ dweight, void* __restrict__ dlogits) {
+  const int lane = threadIdx.x % 32;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  if (n >= N) return;
+  float v[VPL], d[VPL];
+  bool chosen[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    v[i] = e < E ? load_logit<BF16>(logits, n * E + e) : -INFINITY;
+    d[i] = 0.0f;
+    chosen[i] = false;
+  }
+  const int my_e = lane < k ? __ldg(expert + n * k + lane) : -1;
+  const float my_d = lane < k ? __ldg(dweight + n * k + lane) : 0.0f;
+  for (int j = 0; j < k; ++j) {
+    const int e = __shfl_sync(0xffffffffu, my_e, j);
+    const float g = __shfl_sync(0xffffffffu, my_d, j);
+    if (e < 0) continue;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane + 32 * i == e) {
+        d[i] += g;
+        chosen[i] = true;
+      }
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (gate == TP_GATE_SOFTMAX || chosen[i]) m = fmaxf(m, v[i]);
+  m = warp_max(m);
+  float total = 0.0f, inner = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    v[i] = m > -INFINITY && (gate == TP_GATE_SOFTMAX || chosen[i]) ? expf(v[i] - m) : 0.0f;
+    total += v[i];
+    inner += v[i] * d[i];
+  }
+  total = warp_sum(total);
+  inner = warp_sum(inner);
+  const float r = total > 0.0f ? 1.0f / total : 0.0f;
+  inner *= r;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    if (e >= E) continue;
+    const float g = v[i] > 0.0f ? v[i] * r * (d[i] - inner) : 0.0f;
+    if constexpr (BF16)
+      static_cast<uint16_t*>(dlogits)[n * E + e] = to_bf(g);
+    else
+      static_cast<float*>(dlogits)[n * E + e] = g;
+  }
+}
+
+// ------------------------------------------------------------------ combine
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float (&f)[8]) {
+  if constexpr (BF16) {
+    unpack_bf8(ld_nc_v4(static_cast<const uint16_t*>(base) + at), f);
+  } else {
+    const uint4 a = ld_nc_v4(static_cast<const float*>(base) + at);
+    const uint4 b = ld_nc_v4(static_cast<const float*>(base) + at + 4);
+    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+  }
+}
+
+template <int KMAX, bool U_BF16, bool Y_BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u, int64_t R, const float* __restrict__ weight,
+                                                      const int32_t* __restrict__ slot, int64_t N, int h, int k,
+                                                      void* __restrict__ y) {
+  const int per_row = h / 8;
+  const int64_t items = N * per_row;
+  for (int64_t it = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; it < items;
+       it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t n = it / per_row;
+    const int col = static_cast<int>(it - n * per_row) * 8;
+    float acc[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += KMAX) {
+      float f[KMAX][8];
+      float w[KMAX];
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        const int s = j0 + j < k ? __ldg(slot + n * k + j0 + j) : -1;
+        const bool in = s >= 0 && s < R;
+        w[j] = !in ? 0.0f : weight != nullptr ? __ldg(weight + n * k + j0 + j) : 1.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[j][q] = 0.0f;
+        if (in) load8<U_BF16>(u, static_cast<int64_t>(s) * h + col, f[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], f[j][q], acc[q]);
+    }
+    if constexpr (Y_BF16) {
+      st_v4(static_cast<uint16_t*>(y) + n * h + col, pack_bf8(acc));
+    } else {
+      float* o = static_cast<float*>(y) + n * h + col;
+      st_v4(o, make_uint4(__float_as_uint(acc[0]), __float_as_uint(acc[1]), __float_as_uint(acc[2]), __float_as_uint(acc[3])));
+      st_v4(o + 4, make_uint4(__float_as_uint(acc[4]), __float_as_uint(acc[5]), __float_as_uint(acc[6]), __float_as_uint(acc[7])));
+    }
+  }
+}
+
+template <int KMAX, bool DY_BF16, bool U_BF16>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ u, int64_t R,
+                                                          const float* __restrict__ weight, const int32_t* __restrict__ slot,
+                                                          int64_t N, int h, int k, uint16_t* __restrict__ du,
+                                                          float* __restrict__ dweight) {
+  const int lane = threadIdx.x % 32;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  if (n >= N) return;
+  int s[KMAX];
+  float w[KMAX], dot[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    s[j] = j < k ? __ldg(slot + n * k + j) : -1;
+    if (s[j] >= R) s[j] = -1;
+    w[j] = s[j] >= 0 ? __ldg(weight + n * k + j) : 0.0f;
+    dot[j] = 0.0f;
+  }
+  for (int col = lane * 8; col < h; col += 256) {
+    float g[8];
+    load8<DY_BF16>(dy, n * h + col, g);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (s[j] < 0) continue;
+      const int64_t at = static_cast<int64_t>(s[j]) * h + col;
+      float f[8], o[8];
+      load8<U_BF16>(u, at, f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        dot[j] = fmaf(g[q], f[q], dot[j]);
+        o[q] = w[j] * g[q];
+      }
+      st_v4(du + at, pack_bf8(o));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    const float t = warp_sum(dot[j]);
+    if (lane == 0 && j < k) dweight[n * k + j] = t;
+  }
+}
+
+// ------------------------------------------------------------------ launches
+template <bool BF16>
+tp_status launch_route(const void* logits, int gate, float* weight, const SortParams& p, cudaStream_t s) {
+  const size_t smem = (static_cast<size_t>(p.E) * WORDS + p.E + 1) * 4;
+  const int vpl = (p.E + 31) / 32;
+  if (vpl <= 2) route_kernel<2, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
+  else if (vpl <= 4) route_kernel<4, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
+  else if (vpl <= 8) route_kernel<8, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
+  else route_kernel<32, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
+  return check_launch("route_kernel");
+}
+
+template <bool BF16>
+tp_status launch_route_bwd(const void* logits, int64_t N, int E, int k, int gate, const int32_t* expert,
+                           const float* dweight, void* dlogits, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((N + 7) / 8);
+  const int vpl = (E + 31) / 32;
+  if (vpl <= 2) route_bwd_kernel<2, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
+  else if (vpl <= 4) route_bwd_kernel<4, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
+  else if (vpl <= 8) route_bwd_kernel<8, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
+  else route_bwd_kernel<32, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
+  return check_launch("route_bwd_kernel");
+}
+
+// Offsets and places of a batch of more than one block, from the counts of its blocks.
+tp_status scan_and_place(const SortParams& p, cudaStream_t s) {
+  const int buckets = p.E + p.rest;
+  sort_scan_kernel<<<(buckets + 7) / 8, 256, 0, s>>>(p);
+  if (tp_status st = check_launch("sort_scan_kernel")) return st;
+  sort_place_kernel<<<p.blocks, 256, (static_cast<size_t>(buckets) * WORDS + buckets + 1) * 4, s>>>(p);
+  return check_launch("sort_place_kernel");
+}
+
+int64_t sort_blocks(int64_t N) { return (N + TB - 1) / TB; }
+size_t sort_ws_bytes(int64_t N, int64_t buckets) {
+  const int64_t b = sort_blocks(N);
+  return b > 1 ? static_cast<size_t>(buckets) * (b + 1) * 4 : 0;
+}
+
+template <int KMAX, bool U_BF16>
+tp_status launch_combine(const void* u, int64_t R, const float* weight, const int32_t* slot, int64_t N, int h, int k,
+                         void* y, bool y_bf16, cudaStream_t s) {
+  const int64_t blocks = (N * (h / 8) + 255) / 256;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
+  if (cap <= 0) return fail(TP_ECUDA, "cannot query the SM count");
+  const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
+  if (y_bf16) combine_kernel<KMAX, U_BF16, true><<<grid, 256, 0, s>>>(u, R, weight, slot, N, h, k, y);
+  else combine_kernel<KMAX, U_BF16, false><<<grid, 256, 0, s>>>(u, R, weight, slot, N, h, k, y);
+  return check_launch("combine_kernel");
+}
+
+template <int KMAX>
+tp_status launch_combine_bwd(const void* dy, bool dy_bf16, const void* u, bool u_bf16, int64_t R, const float* weight,
+                             const int32_t* slot, int64_t N, int h, int k, uint16_t* du, float* dweight, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((N + 7) / 8);
+  if (dy_bf16 && u_bf16)
+    combine_bwd_kernel<KMAX, true, true><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
+  else if (dy_bf16)
+    combine_bwd_kernel<KMAX, true, false><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
+  else if (u_bf16)
+    combine_bwd_kernel<KMAX, false, true><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
+  else
+    combine_bwd_kernel<KMAX, false, false><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
+  return check_launch("combine_bwd_kernel");
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool valid_dtype(tp_dtype d) { return d == TP_F32 || d == TP_BF16; }
+bool valid_act(tp_act a) { return a == TP_ACT_NONE || a == TP_ACT_GELU || a == TP_ACT_GELU_TANH || a == TP_ACT_SWIGLU; }
+constexpr int64_t MAX_SIZE = INT32_MAX / 4;        // rows and columns: tile coordinates stay in 32 bits
+
+tp_status check_route(int64_t N, int E, int k, tp_gate gate, tp_dtype dtype) {
+  if (N < 0 || E <= 0 || k <= 0) return fail(TP_EINVAL, "negative size, or no experts");
+  if (!valid_dtype(dtype)) return fail(TP_EINVAL, "bad dtype");
+  if (gate != TP_GATE_SOFTMAX && gate != TP_GATE_TOPK) return fail(TP_EINVAL, "bad gate %d", static_cast<int>(gate));
+  if (E > TP_MAX_EXPERTS) return fail(TP_EUNSUPPORTED, "%d experts: at most %d", E, TP_MAX_EXPERTS);
+  if (k > TP_MAX_TOPK) return fail(TP_EUNSUPPORTED, "k=%d: at most %d experts for a token", k, TP_MAX_TOPK);
+  if (k > E) return fail(TP_ESHAPE, "k=%d exceeds the %d experts", k, E);
+  if (N > MAX_SIZE / k) return fail(TP_ESHAPE, "too many tokens");
+  return TP_OK;
+}
+
+// Sizes and pointers that the three ragged products share. y/dy rows: R; x rows: x_rows.
+tp_status check_ragged(int64_t x_rows, const int32_t* row_index, int64_t R, int E, int64_t k, int64_t n) {
+  if (x_rows < 0 || R < 0 || E <= 0 || k <= 0 || n <= 0) return fail(TP_EINVAL, "negative size or empty contraction");
+  if (E > TP_MAX_EXPERTS) return fail(TP_EUNSUPPORTED, "%d segments: at most %d", E, TP_MAX_EXPERTS);
+  if (x_rows > MAX_SIZE || R > MAX_SIZE || k > MAX_SIZE || n > MAX_SIZE) return fail(TP_ESHAPE, "size too large");
+  if (row_index == nullptr && x_rows < R) return fail(TP_ESHAPE, "x has %lld rows for %lld", (long long)x_rows, (long long)R);
+  if (k % 8 || n % 8) return fail(TP_EALIGN, "k and n must be multiples of 8");
+  return TP_OK;
+}
+
+}  // namespace
+}  // namespace tpx
+
+using namespace tpx;
+
+extern "C" {
+
+size_t tp_moe_route_ws_bytes(int64_t N, int E, int k) {
+  if (N <= 0 || E <= 0 || E > TP_MAX_EXPERTS || k <= 0 || N > MAX_SIZE) return 0;
+  return sort_ws_bytes(N, E);
+}
+
+tp_status tp_moe_route(const void* logits, tp_dtype dtype, int64_t N, int E, int k, tp_gate gate, int32_t* expert,
+                       float* weight, int32_t* slot, int32_t* offsets, int32_t* row_token, void* ws, size_t ws_bytes,
+                       void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tp_status st = check_route(N, E, k, gate, dtype)) return st;
+  if (N == 0) return TP_OK;
+  if (!logits || !expert || !weight || !slot || !offsets || !row_token) return fail(TP_EINVAL, "null pointer");
+  if (!aligned4(expert) || !aligned4(weight) || !aligned4(slot) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(ws) ||
+      (dtype == TP_F32 && !aligned4(logits)) || (reinterpret_cast<uintptr_t>(logits) & 1u))
+    return fail(TP_EALIGN, "pointer not aligned to its elements");
+  const size_t need = tp_moe_route_ws_bytes(N, E, k);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  SortParams p = {N, E, k, 0, static_cast<int>(sort_blocks(N)), expert, slot, offsets, row_token, static_cast<int32_t*>(ws)};
+  if (tp_status st = dtype == TP_BF16 ? launch_route<true>(logits, gate, weight, p, s) : launch_route<false>(logits, gate, weight, p, s))
+    return st;
+  return p.blocks == 1 ? TP_OK : scan_and_place(p, s);
+}
+
+tp_status tp_moe_route_bwd(const void* logits, tp_dtype dtype, int64_t N, int E, int k, tp_gate gate, const int32_t* expert,
+                           const float* dweight, void* dlogits, void* stream) {
+  if (tp_status st = check_route(N, E, k, gate, dtype)) return st;
+  if (N == 0) return TP_OK;
+  if (!logits || !expert || !dweight || !dlogits) return fail(TP_EINVAL, "null pointer");
+  const uintptr_t mask = dtype == TP_F32 ? 3u : 1u;
+  if (!aligned4(expert) || !aligned4(dweight) || (reinterpret_cast<uintptr_t>(logits) & mask) ||
+      (reinterpret_cast<uintptr_t>(dlogits) & mask))
+    return fail(TP_EALIGN, "pointer not aligned to its elements");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dtype == TP_BF16 ? launch_route_bwd<true>(logits, N, E, k, gate, expert, dweight, dlogits, s)
+                          : launch_route_bwd<false>(logits, N, E, k, gate, expert, dweight, dlogits, s);
+}
+
+tp_status tp_ragged_linear(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const int32_t* offsets, int64_t R,
+                           int E, int64_t k, int64_t n, tp_act act, const uint16_t* w, void* y, tp_dtype y_dtype,
+                           uint16_t* pre, void* stream) {
+  if (tp_status st = check_ragged(x_rows, row_index, R, E, k, n)) return st;
+  if (!valid_act(act) || !valid_dtype(y_dtype)) return fail(TP_EINVAL, "bad activation or dtype");
+  if (act == TP_ACT_NONE && pre != nullptr) return fail(TP_EINVAL, "pre is the activation's input: there is no activation");
+  if (R == 0) return TP_OK;
+  if (!x || !offsets || !w || !y) return fail(TP_EINVAL, "null pointer");
+  if (x_rows == 0) return fail(TP_ESHAPE, "x has no rows");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(pre)) return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(offsets) || !aligned4(row_index)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  RaggedArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.x = x; g.x_rows = x_rows; g.row_index = row_index; g.offsets = offsets; g.R = R; g.E = E; g.K = k; g.n = n;
+  g.w = w; g.act = act; g.y = y; g.out_f32 = y_dtype == TP_F32; g.pre = pre;
+  return ragged_product(g, static_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_ragged_linear_dx(const uint16_t* dy, const int32_t* offsets, int64_t R, int E, int64_t k, int64_t n,
+                              const uint16_t* w, tp_act act, const uint16_t* h_pre, uint16_t* dx, void* stream) {
+  if (tp_status st = check_ragged(R, nullptr, R, E, k, n)) return st;
+  if (!valid_act(act)) return fail(TP_EINVAL, "bad activation");
+  if (R == 0) return TP_OK;
+  if (!dy || !offsets || !w || !dx) return fail(TP_EINVAL, "null pointer");
+  if ((act != TP_ACT_NONE) != (h_pre != nullptr)) return fail(TP_EINVAL, "h_pre is given exactly with an activation");
+  if (!aligned16(dy) || !aligned16(w) || !aligned16(dx) || !aligned16(h_pre)) return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(offsets)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  RaggedArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.x = dy; g.x_rows = R; g.offsets = offsets; g.R = R; g.E = E; g.K = n; g.n = k;
+  g.w = w; g.w_km = true; g.act = act; g.backward = true; g.h_pre = h_pre; g.y = dx;
+  return ragged_product(g, static_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_ragged_linear_dw(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const uint16_t* dy,
+                              const int32_t* offsets, int64_t R, int E, int64_t k, int64_t n, void* dw, tp_dtype dw_dtype,
+                              void* stream) {
+  if (tp_status st = check_ragged(x_rows, row_index, R, E, k, n)) return st;
+  if (!valid_dtype(dw_dtype)) return fail(TP_EINVAL, "bad dtype");
+  if (!offsets || !dw) return fail(TP_EINVAL, "null pointer");
+  if (R > 0 && (!x || !dy)) return fail(TP_EINVAL, "null pointer");
+  if (R > 0 && x_rows == 0) return fail(TP_ESHAPE, "x has no rows");
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(dw)) return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(offsets) || !aligned4(row_index)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (R == 0) {                                   // no rows: every gradient is zero
+    if (cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * k * n * (dw_dtype == TP_F32 ? 4 : 2), s) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot clear the weight gradients");
+    return TP_OK;
+  }
+  const RaggedDwArgs g = {x, x_rows, row_index, dy, offsets, R, E, k, n, dw, dw_dtype == TP_F32};
+  return ragged_dw(g, s);
+}
+
+tp_status tp_moe_combine(const void* u, tp_dtype u_dtype, int64_t R, const float* weight, const int32_t* slot, int64_t N,
+                         int64_t h, int k, void* y, tp_dtype y_dtype, void* stream) {
+  if (N < 0 || R < 0 || h <= 0 || k <= 0) return fail(TP_EINVAL, "negative size");
+  if (!valid_dtype(u_dtype) || !valid_dtype(y_dtype)) return fail(TP_EINVAL, "bad dtype");
+  if (k > TP_MAX_TOPK) return fail(TP_EUNSUPPORTED, "k=%d: at most %d experts for a token", k, TP_MAX_TOPK);
+  if (N > MAX_SIZE / k || R > MAX_SIZE || h > MAX_SIZE) return fail(TP_ESHAPE, "size too large");
+  if (h % 8) return fail(TP_EALIGN, "h must be a multiple of 8");
+  if (N == 0) return TP_OK;
+  if (!slot || !y || (R > 0 && !u)) return fail(TP_EINVAL, "null pointer");
+  if (!aligned16(u) || !aligned16(y)) return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(weight) || !aligned4(slot)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool yb = y_dtype == TP_BF16;
+  const int hh = static_cast<int>(h);
+  if (u_dtype == TP_BF16) {
+    if (k <= 2) return launch_combine<2, true>(u, R, weight, slot, N, hh, k, y, yb, s);
+    if (k <= 4) return launch_combine<4, true>(u, R, weight, slot, N, hh, k, y, yb, s);
+    return launch_combine<8, true>(u, R, weight, slot, N, hh, k, y, yb, s);
+  }
+  if (k <= 2) return launch_combine<2, false>(u, R, weight, slot, N, hh, k, y, yb, s);
+  return launch_combine<4, false>(u, R, weight, slot, N, hh, k, y, yb, s);
+}
+
+tp_status tp_moe_combine_bwd(const void* dy, tp_dtype dy_dtype, const void* u, tp_dtype u_dtype, int64_t R,
+                             const float* weight, const int32_t* slot, int64_t N, int64_t h, int k, uint16_t* du,
+                             float* dweight, void* stream) {
+  if (N < 0 || R < 0 || h <= 0 || k <= 0) return fail(TP_EINVAL, "negative size");
+  if (!valid_dtype(u_dtype) || !valid_dtype(dy_dtype)) return fail(TP_EINVAL, "bad dtype");
+  if (k > TP_MAX_TOPK) return fail(TP_EUNSUPPORTED, "k=%d: at most %d experts for a token", k, TP_MAX_TOPK);
+  if (N > MAX_SIZE / k || R > MAX_SIZE || h > MAX_SIZE) return fail(TP_ESHAPE, "size too large");
+  if (h % 8) return fail(TP_EALIGN, "h must be a multiple of 8");
+  if (N == 0) return TP_OK;
+  if (!dy || !weight || !slot || !dweight || (R > 0 && (!u || !du))) return fail(TP_EINVAL, "null pointer");
+  if (!aligned16(dy) || !aligned16(u) || !aligned16(du)) return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(weight) || !aligned4(slot) || !aligned4(dweight)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool db = dy_dtype == TP_BF16, ub = u_dtype == TP_BF16;
+  const int hh = static_cast<int>(h);
+  if (k <= 2) return launch_combine_bwd<2>(dy, db, u, ub, R, weight, slot, N, hh, k, du, dweight, s);
+  if (k <= 8) return launch_combine_bwd<8>(dy, db, u, ub, R, weight, slot, N, hh, k, du, dweight, s);
+  return launch_combine_bwd<TP_MAX_TOPK>(dy, db, u, ub, R, weight, slot, N, hh, k, du, dweight, s);
+}
+
+size_t tp_moe_mlp_ws_bytes(int64_t N, int E, int k) { return tp_moe_route_ws_bytes(N, E, k); }
+
+tp_status tp_moe_mlp_fwd(const uint16_t* x, int64_t N, int64_t h, int64_t F, int E, int k, tp_gate gate, tp_act act,
+                         const void* logits, tp_dtype logits_dtype, const uint16_t* w_in, const uint16_t* w_down,
+                         int32_t* expert, float* weight, int32_t* slot, int32_t* offsets, int32_t* row_token,
+                         uint16_t* h_pre, uint16_t* z, uint16_t* u, void* y, tp_dtype y_dtype, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (tp_status st = check_route(N, E, k, gate, logits_dtype)) return st;
+  if (tp_status st = check_ragged(N, nullptr, N, E, h, F)) return st;
+  if (!valid_act(act) || !valid_dtype(y_dtype)) return fail(TP_EINVAL, "bad activation or dtype");
+  if (N == 0) return TP_OK;
+  if (!x || !logits || !w_in || !w_down || !expert || !weight || !slot || !offsets || !row_token || !z || !u || !y)
+    return fail(TP_EINVAL, "null pointer");
+  if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(h_pre) || !aligned16(z) || !aligned16(u) || !aligned16(y))
+    return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (act == TP_ACT_NONE && h_pre != nullptr) return fail(TP_EINVAL, "h_pre is the activation's input: there is no activation");
+  const int64_t R = N * k;
+  if (tp_status st = tp_moe_route(logits, logits_dtype, N, E, k, gate, expert, weight, slot, offsets, row_token, ws, ws_bytes, stream))
+    return st;
+  if (tp_status st = tp_ragged_linear(x, N, row_token, offsets, R, E, h, F, act, w_in, z, TP_BF16, h_pre, stream)) return st;
+  if (tp_status st = tp_ragged_linear(z, R, nullptr, offsets, R, E, F, h, TP_ACT_NONE, w_down, u, TP_BF16, nullptr, stream)) return st;
+  return tp_moe_combine(u, TP_BF16, R, weight, slot, N, h, k, y, y_dtype, stream);
+}
+
+tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64_t h, int64_t F, int E, int k, tp_gate gate,
+                         tp_act act, const void* logits, tp_dtype logits_dtype, const uint16_t* w_in,
+                         const uint16_t* w_down, const int32_t* expert, const float* weight, const int32_t* slot,
+                         const int32_t* offsets, const int32_t* row_token, const uint16_t* h_pre, const uint16_t* z,
+                         const uint16_t* u, uint16_t* du_ws, uint16_t* dh_ws, float* dweight_ws, float* dw_in,
+                         float* dw_down, void* dx, tp_dtype dx_dtype, void* dlogits, void* stream) {
+  if (tp_status st = check_route(N, E, k, gate, logits_dtype)) return st;
+  if (tp_status st = check_ragged(N, nullptr, N, E, h, F)) return st;
+  if (!valid_act(act) || !valid_dtype(dx_dtype)) return fail(TP_EINVAL, "bad activation or dtype");
+  if (N > 0 && (!x || !dy || !logits || !w_in || !w_down || !expert || !weight || !slot || !row_token || !z || !u || !du_ws ||
+                !dh_ws || !dweight_ws || !dx || !dlogits))
+    return fail(TP_EINVAL, "null pointer");
+  if (!offsets || !dw_in || !dw_down) return fail(TP_EINVAL, "null pointer");
+  if (N > 0 && (act != TP_ACT_NONE) != (h_pre != nullptr)) return fail(TP_EINVAL, "h_pre is given exactly with an activation");
+  if (!aligned16(x) || !aligned16(dy) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(h_pre) || !aligned16(z) ||
+      !aligned16(u) || !aligned16(du_ws) || !aligned16(dh_ws) || !aligned16(dw_in) || !aligned16(dw_down) || !aligned16(dx))
+    return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  const int64_t R = N * k, wn = act == TP_ACT_SWIGLU ? 2 * F : F;
+  // combine -> down (both gradients) -> activation (in the down product's epilogue) -> up (both) -> tokens
+  if (tp_status st = tp_moe_combine_bwd(dy, TP_BF16, u, TP_BF16, R, weight, slot, N, h, k, du_ws, dweight_ws, stream)) return st;
+  if (tp_status st = tp_moe_route_bwd(logits, logits_dtype, N, E, k, gate, expert, dweight_ws, dlogits, stream)) return st;
+  if (tp_status st = tp_ragged_linear_dw(z, R, nullptr, du_ws, offsets, R, E, F, h, dw_down, TP_F32, stream)) return st;
+  if (tp_status st = tp_ragged_linear_dx(du_ws, offsets, R, E, F, h, w_down, act, h_pre, dh_ws, stream)) return st;
+  if (tp_status st = tp_ragged_linear_dw(x, N, row_token, dh_ws, offsets, R, E, h, wn, dw_in, TP_F32, stream)) return st;
+  if (N == 0) return TP_OK;
+  // every row's gradient of x takes the place of du, which is not needed any more
+  if (tp_status st = tp_ragged_linear_dx(dh_ws, offsets, R, E, h, wn, w_in, TP_ACT_NONE, nullptr, du_ws, stream)) return st;
+  return tp_moe_combine(du_ws, TP_BF16, R, nullptr, slot, N, h, k, dx, dx_dtype, stream);
+}
+
+size_t tp_lora_plan_ws_bytes(int64_t N, int L) {
+  if (N <= 0 || L <= 0 || L > TP_MAX_EXPERTS || N > MAX_SIZE) return 0;
+  return sort_ws_bytes(N, L + 1);
+}
+
+tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, int32_t* row_token, void* ws, size_t ws_bytes,
+                       void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N < 0 || L <= 0) return fail(TP_EINVAL, "negative size, or no adapters");
+  if (L > TP_MAX_EXPERTS) return fail(TP_EUNSUPPORTED, "%d adapters: at most %d", L, TP_MAX_EXPERTS);
+  if (N > MAX_SIZE) return fail(TP_ESHAPE, "too many tokens");
+  if (N == 0) return TP_OK;
+  if (!id || !offsets || !row_token) return fail(TP_EINVAL, "null pointer");
+  if (!aligned4(id) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(ws)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  const size_t need = tp_lora_plan_ws_bytes(N, L);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  SortParams p = {N, L, 1, 1, static_cast<int>(sort_blocks(N)), const_cast<int32_t*>(id), nullptr, offsets, row_token,
+                  static_cast<int32_t*>(ws)};
+  sort_count_kernel<<<p.blocks, 256, (static_cast<size_t>(L + 1) * WORDS + L + 2) * 4, s>>>(p);
+  if (tp_status st = check_launch("sort_count_kernel")) return st;
+  return p.blocks == 1 ? TP_OK : scan_and_place(p, s);
+}
+
+size_t tp_lora_ws_bytes(int64_t N, int rank) {
+  if (N <= 0 || rank <= 0 || N > MAX_SIZE) return 0;
+  return static_cast<size_t>(N) * rank * 4;
+}
+
+tp_status tp_lora_linear(const uint16_t* x, int64_t N, int64_t k, int64_t n, int t, const uint16_t* w, int L, int rank,
+                         const uint16_t* a, const uint16_t* b, const float* scale, const int32_t* offsets,
+                         const int32_t* row_token, uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!valid_t(t)) return fail(TP_EINVAL, "t=%d outside 1..%d", t, TP_MAX_SHARDS);
+  if (N < 0 || k <= 0 || n <= 0 || L <= 0 || rank <= 0) return fail(TP_EINVAL, "negative size, empty contraction or no adapters");
+  if (L > TP_MAX_EXPERTS) return fail(TP_EUNSUPPORTED, "%d adapters: at most %d", L, TP_MAX_EXPERTS);
+  if (n % t) return fail(TP_EDIVIS, "t=%d does not divide n=%lld", t, (long long)n);
+  if (N > MAX_SIZE || k > MAX_SIZE || n > MAX_SIZE || rank > MAX_SIZE) return fail(TP_ESHAPE, "size too large");
+  if (k % 8 || (n / t) % 8 || rank % 8) return fail(TP_EALIGN, "k, n/t and rank must be multiples of 8");
+  if (N == 0) return TP_OK;
+  if (!x || !w || !a || !b || !offsets || !row_token || !y) return fail(TP_EINVAL, "null pointer");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(a) || !aligned16(b) || !aligned16(y) || !aligned16(ws))
+    return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(scale) || !aligned4(offsets) || !aligned4(row_token)) return fail(TP_EALIGN, "pointer not aligned to its elements");
+  const size_t need = tp_lora_ws_bytes(N, rank);
+  if (ws == nullptr || ws_bytes < need) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  RaggedArgs g;                                    // v = scale * x A over the adapters' segments, binary32
+  std::memset(&g, 0, sizeof(g));
+  g.x = x; g.x_rows = N; g.row_index = row_token; g.offsets = offsets; g.R = N; g.E = L; g.K = k; g.n = rank;
+  g.w = a; g.act = TP_ACT_NONE; g.y = ws; g.out_f32 = true; g.seg_scale = scale;
+  if (tp_status st = ragged_product(g, s)) return st;
+  std::memset(&g, 0, sizeof(g));                   // y[r] = x W[r] + v B[r]
+  g.x = x; g.x_rows = N; g.row_index = row_token; g.offsets = offsets; g.R = N; g.E = t; g.K = k; g.n = n / t;
+  g.w = w; g.act = TP_ACT_NONE; g.y = y; g.v = static_cast<const float*>(ws); g.lora_b = b; g.L = L; g.rank = rank;
+  return ragged_product(g, s);
+}
+
+}  // extern "C"

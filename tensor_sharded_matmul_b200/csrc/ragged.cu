@@ -1,0 +1,415 @@
+// Matrix products over ragged segments of rows: y_i = epilogue(x[row_i] W_e) for the rows i of every
+// segment e, the segments known on the device alone (an expert's tokens, an adapter's tokens).
+//
+// The product is computed transposed, D^T = W_e^T x^T: 128 columns of W are the M of
+// tcgen05.mma and the segment's rows are its N, which is chosen for each tile in steps of 16. A
+// segment's last tile so costs what its rows cost, and a decode step's few rows need no padding to
+// 128. W as stored ([K][n], n contiguous) is the M-major operand, the rows of x the K-major one; both
+// come by TMA, x's rows four at a time by index (tile::gather4), so that gathered rows are never
+// copied. One CTA computes one tile: warp 0 loads, one thread of warp 1 issues the MMAs, all warps
+// write the output rows.
+//
+// With few tiles the contraction is split over the CTAs of a cluster. Each leaves its partial tile in
+// its shared memory; the cluster then sums the partials in rank order (no atomics: results do not
+// depend on timing) and writes the rows, each CTA a share of them.
+//
+// Adapters (y = x W + s_a (x A_a) B_a): the rows are the tokens sorted by adapter, v = s_a x A_a comes
+// from a first product over the adapters' segments, and v B_a is accumulated into the same TMEM tile
+// as further k-blocks: 16 ranks of one adapter are one MMA step, whose x-side operand holds v for the
+// tokens of that adapter and zeros for the others. v is held in binary32 and enters as two bf16
+// numbers (v = hi + lo, |v - hi - lo| <= 2^-16 |v|), so that nothing is rounded to bf16 between the two
+// products.
+#include <cstring>
+
+#include "ragged.cuh"
+#include "tmap.cuh"
+
+namespace tpx {
+namespace {
+
+constexpr int BM = 128;                       // columns of W per tile (the MMA's M)
+constexpr int BK = 64;                        // one 128-byte swizzle atom of bf16
+constexpr int STAGES = 4;
+constexpr uint32_t W_STAGE = BM * BK * 2;     // 16 KiB
+constexpr uint32_t W_BOX = 64 * BK * 2;       // 64 columns x 64 k: 8 KiB
+constexpr int THREADS = 192;                  // loads, MMA, 4 warps that read TMEM
+constexpr int STG_LD = BM + 4;                // floats between rows of the staged output tile
+constexpr int MAX_SEGS = TP_MAX_EXPERTS;
+
+template <int NT>
+constexpr size_t smem_bytes() {
+  return 1024 + STAGES * (W_STAGE + NT * BK * 2) + (2 * STAGES + 4) * 8 + 16 + (MAX_SEGS + 4) * 4 + 2 * NT * 4;
+}
+
+template <int NT, bool SWIGLU, bool LORA>
+__global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__ RaggedParams p) {
+  static_assert(NT * STG_LD * 4 <= STAGES * (W_STAGE + NT * BK * 2), "the staged output tile reuses the operand stages");
+  constexpr uint32_t X_STAGE = NT * BK * 2;
+  constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_w = smem;
+  uint8_t* s_x = smem + STAGES * W_STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_x + STAGES * X_STAGE);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
+  const uint32_t accf = empty0 + 8 * STAGES, drain = accf + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int* s_count = reinterpret_cast<int*>(tmem_slot + 2);            // adapters of this tile
+  int* s_off = reinterpret_cast<int*>(bars + 2 * STAGES + 4) + 4;  // 16-byte aligned
+  int* s_idx = s_off + MAX_SEGS + 4;
+  int* s_list = s_idx + NT;
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&p.tw);
+    prefetch_tmap(&p.tx);
+    if (SWIGLU) prefetch_tmap(&p.tw2);
+    if (LORA) prefetch_tmap(&p.tb);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(accf, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  const int segs = LORA ? p.L : p.E;
+  for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  // This cluster's tile: segment (adapters: shard) e, rows i0 .. i0 + valid - 1, columns n0 ...
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / p.split;
+  int e, i0, valid, ct;
+  bool live;
+  if (LORA) {
+    const int row_tiles = (p.R + NT - 1) / NT;
+    const int rt = unit % row_tiles;
+    ct = unit / row_tiles;
+    e = ct / p.tiles_n;
+    ct -= e * p.tiles_n;
+    i0 = rt * NT;
+    valid = min(NT, p.R - i0);
+    live = e < p.E;
+  } else {
+    const SegTile t = find_seg_tile<NT>(s_off, p.E, unit / p.tiles_n, lane);
+    live = t.live;
+    e = t.e;
+    const int local = unit - t.before * p.tiles_n;
+    const int rt = live ? local % t.count : 0;
+    ct = live ? local / t.count : 0;
+    i0 = s_off[e] + rt * NT;
+    valid = min(NT, s_off[e + 1] - i0);
+  }
+  constexpr int TILE_N = SWIGLU ? BM / 2 : BM;       // output columns per tile
+  const int n0 = ct * TILE_N;
+
+  if (live) {
+    // x's row of every row of the tile; -1: the index lies outside x (the row reads as zeros)
+    for (int j = threadIdx.x; j < ((valid + 3) & ~3); j += THREADS) {
+      const int i = i0 + min(j, valid - 1);
+      const int r = p.row_index != nullptr ? __ldg(p.row_index + i) : i;
+      s_idx[j] = r >= 0 && r < p.x_rows ? r : -1;
+    }
+    if (LORA && warp == 2) {                         // the adapters that own rows of this tile, ascending
+      int n_list = 0;
+      for (int a0 = 0; a0 < p.L; a0 += 32) {
+        const int a = a0 + lane;
+        const bool in = a < p.L && max(s_off[a], i0) < min(s_off[a + 1], i0 + valid);
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        const int at = n_list + __popc(m & ((1u << lane) - 1));
+        if (in && at < NT) s_list[at] = a;
+        n_list += __popc(m);
+      }
+      if (lane == 0) *s_count = min(n_list, NT);
+    }
+  }
+  __syncthreads();
+
+  const int per_adapter = LORA ? (p.rank + 15) / 16 : 1;            // 16-rank steps of one adapter
+  const int chunks = LORA && live ? *s_count * per_adapter : 0;
+  const int total_kb = p.num_kb + (chunks + 1) / 2;                 // two adapter steps per k-block
+  const int kb0 = live ? static_cast<int>(static_cast<int64_t>(total_kb) * rank / p.split) : 0;
+  const int kb1 = live ? static_cast<int>(static_cast<int64_t>(total_kb) * (rank + 1) / p.split) : 0;
+  const int n_mma = live ? (valid + 15) & ~15 : 16;
+  int loaded = 0;                                                   // warp 0: k-blocks loaded
+  bool mma_issued = false;
+
+  if (warp == 0 && live) {
+    const int groups = (valid + 3) / 4;                             // four rows of x per load
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int st = loaded % STAGES;
+      bool ok = mbar_wait_bounded(empty0 + 8 * st, ((loaded / STAGES) & 1) ^ 1, p.budget, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (!*abort_flag) record_timeout(p.status, WAIT_PRODUCER_EMPTY);
+        *abort_flag = 1u;
+        break;
+      }
+      const uint32_t fb = full0 + 8 * st;
+      const uint32_t w_dst = smem_u32(s_w + st * W_STAGE), x_dst = smem_u32(s_x + st * X_STAGE);
+      if (!LORA || kb < p.num_kb) {
+        const int k0 = kb * BK;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(fb, W_STAGE + groups * 512u);
+          if (p.w_km) {
+            tma_load_3d(w_dst, &p.tw, k0, n0, e, fb);
+          } else {
+            tma_load_3d(w_dst, &p.tw, n0, k0, e, fb);
+            tma_load_3d(w_dst + W_BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? n0 : n0 + 64, k0, e, fb);
+          }
+        }
+        __syncwarp();
+        for (int g = lane; g < groups; g += 32) {
+          const int4 r = *reinterpret_cast<const int4*>(s_idx + 4 * g);
+          tma_gather4(x_dst + 512u * g, &p.tx, k0, max(r.x, 0), max(r.y, 0), max(r.z, 0), max(r.w, 0), fb);
+        }
+      } else {
+        // two 16-rank steps: B's rows by TMA, v of the tokens that the adapter owns by this warp
+        const int c0 = 2 * (kb - p.num_kb);
+        for (int it = lane; it < n_mma * 4; it += 32) {
+          const int row = it >> 2, ch = (it >> 1) & 1, sub = it & 1;
+          const int c = c0 + ch;
+          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+          if (c < chunks && row < valid) {
+            const int a = s_list[c / per_adapter];
+            const int r0 = (c % per_adapter) * 16 + sub * 8;
+            const int i = i0 + row;
+            if (i >= s_off[a] && i < s_off[a + 1] && r0 < p.rank) {
+              const float4* src = reinterpret_cast<const float4*>(p.v + static_cast<int64_t>(i) * p.rank + r0);
+              const float4 f0 = src[0], f1 = src[1];
+              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+              float h[8], l[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                h[q] = bf(to_bf(f[q]));
+                l[q] = f[q] - h[q];
+                if (!(fabsf(l[q]) < 1e38f)) l[q] = 0.0f;   // infinite or NaN v: hi alone carries it
+              }
+              hi = pack_bf8(h);
+              lo = pack_bf8(l);
+            }
+          }
+          uint8_t* line = s_x + st * X_STAGE + row * 128;
+          const int piece = 2 * ch + sub;                  // hi in pieces 0..3, lo in 4..7
+          *reinterpret_cast<uint4*>(line + ((piece ^ (row & 7)) << 4)) = hi;
+          *reinterpret_cast<uint4*>(line + (((piece + 4) ^ (row & 7)) << 4)) = lo;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          const int nch = min(2, chunks - c0);
+          mbar_arrive_expect_tx(fb, nch * 4096u);
+          for (int ch = 0; ch < nch; ++ch) {
+            const int a = s_list[(c0 + ch) / per_adapter];
+            const int r0 = ((c0 + ch) % per_adapter) * 16;
+            tma_load_3d(w_dst + ch * 2048u, &p.tb, n0, r0, e * p.L + a, fb);
+            tma_load_3d(w_dst + ch * 2048u + W_BOX, &p.tb, n0 + 64, r0, e * p.L + a, fb);
+          }
+        }
+        __syncwarp();
+      }
+      ++loaded;
+    }
+  } else if (warp == 1 && lane == 0 && live) {
+    const uint32_t idesc = idesc_bf16_f32(BM, n_mma, !p.w_km, false);
+    int done = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++done) {
+      const int st = done % STAGES;
+      if (!mbar_wait_bounded(full0 + 8 * st, (done / STAGES) & 1, p.budget, abort_flag)) {
+        if (!*abort_flag) record_timeout(p.status, WAIT_MMA_FULL);
+        *abort_flag = 1u;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t w_base = smem_u32(s_w + st * W_STAGE), x_base = smem_u32(s_x + st * X_STAGE);
+      if (!LORA || kb < p.num_kb) {
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) {
+          const uint64_t ad = p.w_km ? smem_desc_sw128(w_base + 32u * k, 16u, 1024u)
+                                     : smem_desc_sw128(w_base + 2048u * k, W_BOX, 1024u);
+          umma_bf16(tmem_base, ad, smem_desc_sw128(x_base + 32u * k, 16u, 1024u), idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+        }
+      } else {
+        const int nch = min(2, chunks - 2 * (kb - p.num_kb));
+        for (int q = 0; q < 2 * nch; ++q) {                // hi and lo of each step against the same rows of B
+          const int ch = q >> 1, half = q & 1;
+          umma_bf16(tmem_base, smem_desc_sw128(w_base + 2048u * ch, W_BOX, 1024u),
+                    smem_desc_sw128(x_base + 32u * (ch + 2 * half), 16u, 1024u), idesc, (kb != kb0 || q != 0) ? 1u : 0u);
+        }
+      }
+      mma_issued = true;
+      umma_commit(empty0 + 8 * st);
+    }
+    umma_commit(accf);
+  } else if (warp >= 2 && live) {
+    // TMEM lane = column of W, TMEM column = row of the tile -> staged [row][column] in shared memory
+    // (the operand stages are free: the commit says that every MMA, and so every load, is done)
+    if (!mbar_wait_bounded(accf, 0, p.budget, abort_flag)) {
+      if (!*abort_flag) record_timeout(p.status, WAIT_EPI_ACC_FULL);
+      *abort_flag = 1u;
+    } else if (!*abort_flag) {
+      tc_fence_after();
+      const int quad = warp & 3;
+      float* stg = reinterpret_cast<float*>(smem) + quad * 32 + lane;
+      for (int j0 = 0; j0 < n_mma; j0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + j0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j0 + j < valid) stg[(j0 + j) * STG_LD] = __uint_as_float(v[j]);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+
+  // Partial tiles staged: the cluster's (or this CTA's) threads sum them and write the rows.
+  if (p.split > 1) cluster_sync(); else __syncthreads();
+  if (live && !*abort_flag) {
+    constexpr int GROUPS = TILE_N / 8;
+    const uint32_t stg = smem_u32(smem);
+    for (int it = rank * THREADS + threadIdx.x; it < valid * GROUPS; it += p.split * THREADS) {
+      const int j = it / GROUPS, c8 = (it % GROUPS) * 8;
+      const int col = n0 + c8;
+      if (col >= p.n) continue;
+      float f[8], u[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = u[q] = 0.0f;
+      for (int s = 0; s < p.split; ++s) {
+        const uint32_t at = stg + (j * STG_LD + c8) * 4;
+        const uint32_t src = p.split > 1 ? mapa_shared(at, s) : at;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 x = ld_cluster_v4(src + 16 * q);
+          f[4 * q] += x.x; f[4 * q + 1] += x.y; f[4 * q + 2] += x.z; f[4 * q + 3] += x.w;
+          if constexpr (SWIGLU) {
+            const float4 z = ld_cluster_v4(src + 256 + 16 * q);
+            u[4 * q] += z.x; u[4 * q + 1] += z.y; u[4 * q + 2] += z.z; u[4 * q + 3] += z.w;
+          }
+        }
+      }
+      const int r = s_idx[j];
+      if (r < 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = u[q] = 0.0f;
+      }
+      if (p.seg_scale != nullptr) {
+        const float sc = __ldg(p.seg_scale + e);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] *= sc;
+      }
+      if constexpr (LORA) {
+        if (r >= 0) store_row8(p, static_cast<int64_t>(e) * p.R + r, col, f, u);
+      } else {
+        store_row8(p, i0 + j, col, f, u);
+      }
+    }
+  }
+  if (p.split > 1) cluster_sync();     // a CTA's shared memory outlives its peers' reads
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag != 0u) {             // a wait ran out: let copies and MMAs in flight land first
+    const unsigned long long drain_budget = 4000000000ull;
+    if (warp == 0 && lane == 0) {
+      for (int s = 0; s < STAGES; ++s) {
+        const int uses = (loaded - s + STAGES - 1) / STAGES;
+        if (uses > 0 && !mbar_wait_bounded(full0 + 8 * s, (uses - 1) & 1, drain_budget, nullptr))
+          record_timeout(p.status, WAIT_TEARDOWN);
+      }
+    }
+    if (warp == 1 && lane == 0 && mma_issued) {
+      umma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, drain_budget, nullptr)) record_timeout(p.status, WAIT_TEARDOWN);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+}
+
+template <int NT, bool SWIGLU, bool LORA>
+tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
+  static int configured_for[64] = {};
+  constexpr size_t smem = smem_bytes<NT>();
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
+  if (dev < 0 || dev >= 64 || !configured_for[dev]) {
+    if (cudaFuncSetAttribute(ragged_kernel<NT, SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", smem);
+    if (dev >= 0 && dev < 64) configured_for[dev] = 1;
+  }
+  if (units * p.split > INT32_MAX) return fail(TP_ESHAPE, "too many tiles");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<NT, SWIGLU, LORA>, p);
+  if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_kernel: %s", cudaGetErrorString(err));
+  return check_launch("ragged_kernel");
+}
+
+}  // namespace
+
+tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
+  RaggedParams p;
+  std::memset(&p, 0, sizeof(p));
+  const bool lora = g.v != nullptr;
+  const bool swiglu = g.act == TP_ACT_SWIGLU && !g.backward;
+  if (g.w_km ? !encode_bf16_3d(&p.tw, g.w, g.K, g.n, g.E, g.K, BK, BM)
+             : !encode_bf16_3d(&p.tw, g.w, g.n, g.K, g.E, swiglu ? 2 * g.n : g.n, 64, BK))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptor of the weights");
+  if (swiglu && !encode_bf16_3d(&p.tw2, g.w + g.n, g.n, g.K, g.E, 2 * g.n, 64, BK))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptor of the up half of the weights");
+  if (!encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
+  if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
+  p.offsets = g.offsets; p.row_index = g.row_index; p.seg_scale = g.seg_scale;
+  p.y = g.y; p.pre = g.pre; p.h_pre = g.h_pre; p.v = g.v;
+  p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
+  p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
+  p.num_kb = static_cast<int>((g.K + BK - 1) / BK);
+  p.L = g.L; p.rank = g.rank;
+  p.act = g.act; p.w_km = g.w_km; p.out_f32 = g.out_f32; p.backward = g.backward; p.scatter = lora;
+  p.status = status_word();
+  p.budget = wait_budget();
+  if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");
+  const int tile_n = swiglu ? BM / 2 : BM;
+  p.tiles_n = static_cast<int>((g.n + tile_n - 1) / tile_n);
+  const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
+  const bool narrow = g.R <= 64 * segs;
+  const int nt = narrow ? 64 : 256;
+  const int64_t row_tiles = lora ? (g.R + nt - 1) / nt : g.R / nt + segs;
+  const int64_t units = row_tiles * p.tiles_n * (lora ? g.E : 1);
+  p.split = 1;
+  const int sms = sm_count();
+  while (p.split < 8 && units * p.split < sms && p.num_kb >= 8 * p.split) p.split *= 2;
+  if (narrow) {
+    if (lora) return launch_ragged<64, false, true>(p, units, s);
+    return swiglu ? launch_ragged<64, true, false>(p, units, s) : launch_ragged<64, false, false>(p, units, s);
+  }
+  if (lora) return launch_ragged<256, false, true>(p, units, s);
+  return swiglu ? launch_ragged<256, true, false>(p, units, s) : launch_ragged<256, false, false>(p, units, s);
+}
+
+}  // namespace tpx

@@ -1,0 +1,190 @@
+// What the kernels over ragged segments of rows share: the launch parameters, the place of a tile
+// among the segments, and the form of the output rows.
+//
+// Rows sorted by segment (expert, adapter) are given by offsets[S + 1] in device memory: segment e
+// holds rows offsets[e] .. offsets[e + 1] - 1. The host never reads them. Every offset is taken as
+// clamped to 0 .. R and a segment that ends before it begins is empty, so that no offsets whatever
+// lead outside a buffer of R rows.
+#pragma once
+
+#include <cuda.h>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace tpx {
+
+// Product y_i = epilogue(x[row_i] W_e) over the rows i of every segment e.
+struct RaggedParams {
+  CUtensorMap tw;             // W: [E][K][n], or [E][n][K] (w_km); the gate half for SwiGLU
+  CUtensorMap tw2;            // SwiGLU: the up half
+  CUtensorMap tx;             // x: [x_rows][K], boxes one row high (gathered rows)
+  CUtensorMap tb;             // adapters: B [t * L][rank][n]
+  const int32_t* offsets;     // [E + 1]; adapters: [L + 1], the segments of the adapters
+  const int32_t* row_index;   // x's row of sorted row i; nullptr: i
+  const float* seg_scale;     // optional factor of every row of segment e
+  void* y;                    // output rows, stride n
+  uint16_t* pre;              // optional: the products before the activation (SwiGLU: [gate | up], stride 2n)
+  const uint16_t* h_pre;      // backward: what the activation was applied to (stride n, SwiGLU 2n)
+  const float* v;             // adapters: scale * x A of sorted row i, [N][rank]
+  int R, x_rows;              // sorted rows, rows of x
+  int E, n, K, num_kb, tiles_n;
+  int L, rank;                // adapters: their number and rank
+  int split;                  // CTAs along the contraction
+  int act;                    // tp_act of the epilogue
+  bool w_km;                  // W stored [E][n][K]
+  bool out_f32;
+  bool backward;              // multiply by the activation's derivative at h_pre
+  bool scatter;               // adapters: write row row_index[i], not row i
+  uint32_t* status;
+  unsigned long long budget;
+};
+
+// Host-side arguments of ragged_product (checked by the entry points).
+struct RaggedArgs {
+  const uint16_t* x;          // [x_rows][K]
+  int64_t x_rows;
+  const int32_t* row_index;   // see RaggedParams
+  const int32_t* offsets;
+  int64_t R;                  // rows of y (adapters: tokens)
+  int E;                      // segments (adapters: shards, each over all R rows)
+  int64_t K, n;
+  const uint16_t* w;
+  bool w_km;
+  int act;
+  bool backward;
+  const uint16_t* h_pre;
+  void* y;
+  bool out_f32;
+  uint16_t* pre;
+  const float* seg_scale;
+  const float* v;             // adapters, or nullptr
+  const uint16_t* lora_b;     // [E][L][rank][n]
+  int L, rank;
+};
+tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
+
+// Host-side arguments of ragged_dw: dw[e] = x_e^T dy_e for every segment.
+struct RaggedDwArgs {
+  const uint16_t* x;          // [x_rows][k]
+  int64_t x_rows;
+  const int32_t* row_index;   // nullptr: row i of x
+  const uint16_t* dy;         // [R][n]
+  const int32_t* offsets;
+  int64_t R;
+  int E;
+  int64_t k, n;
+  void* dw;                   // [E][k][n]
+  bool out_f32;
+};
+tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s);
+
+// offsets[e], clamped to the rows that exist.
+__device__ __forceinline__ int seg_bound(const int32_t* offsets, int e, int R) {
+  return min(max(__ldg(offsets + e), 0), R);
+}
+
+// Tile number g among all segments' row tiles of NT rows (segment ascending): its segment, and the
+// number of tiles before and in that segment. `off`: clamped offsets in shared memory. Whole warp.
+struct SegTile {
+  int e, before, count;
+  bool live;
+};
+template <int NT>
+__device__ __forceinline__ SegTile find_seg_tile(const int* off, int E, int g, int lane) {
+  SegTile s{0, 0, 0, false};
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    const int rows = e < E ? max(off[e + 1] - off[e], 0) : 0;
+    const int cnt = (rows + NT - 1) / NT;
+    int inc = cnt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > g);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s.e = e0 + src;
+      s.count = __shfl_sync(0xffffffffu, cnt, src);
+      s.before = base + __shfl_sync(0xffffffffu, inc, src) - s.count;
+      s.live = true;
+      return s;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return s;
+}
+
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+  return static_cast<uint32_t>(to_bf(lo)) | (static_cast<uint32_t>(to_bf(hi)) << 16);
+}
+__device__ __forceinline__ uint4 pack_bf8(const float (&f)[8]) {
+  return make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
+}
+__device__ __forceinline__ void unpack_bf8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ float apply_act(float x, int act) {
+  return act == TP_ACT_GELU ? gelu_erf(x) : act == TP_ACT_GELU_TANH ? gelu_tanh(x) : x;
+}
+
+// Eight neighbouring columns of one output row: f the products (SwiGLU: the gate's, u the up's), in
+// binary32 until the one rounding at the store.
+__device__ __forceinline__ void store_row8(const RaggedParams& p, int64_t row, int col, float (&f)[8], float (&u)[8]) {
+  if (p.backward) {
+    uint16_t* y = static_cast<uint16_t*>(p.y);
+    if (p.act == TP_ACT_SWIGLU) {
+      float g[8], up[8], dg[8], du[8];
+      unpack_bf8(ld_nc_v4(p.h_pre + row * 2 * p.n + col), g);
+      unpack_bf8(ld_nc_v4(p.h_pre + row * 2 * p.n + p.n + col), up);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = 1.0f / (1.0f + __expf(-g[i]));
+        dg[i] = f[i] * up[i] * (s * (1.0f + g[i] * (1.0f - s)));
+        du[i] = f[i] * (g[i] * s);
+      }
+      st_v4(y + row * 2 * p.n + col, pack_bf8(dg));
+      st_v4(y + row * 2 * p.n + p.n + col, pack_bf8(du));
+      return;
+    }
+    if (p.act != TP_ACT_NONE) {
+      float h[8];
+      unpack_bf8(ld_nc_v4(p.h_pre + row * p.n + col), h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= p.act == TP_ACT_GELU ? gelu_grad(h[i]) : gelu_tanh_grad(h[i]);
+    }
+    st_v4(y + row * p.n + col, pack_bf8(f));
+    return;
+  }
+  if (p.act == TP_ACT_SWIGLU) {
+    if (p.pre != nullptr) {
+      st_v4(p.pre + row * 2 * p.n + col, pack_bf8(f));
+      st_v4(p.pre + row * 2 * p.n + p.n + col, pack_bf8(u));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = silu(f[i]) * u[i];
+  } else if (p.act != TP_ACT_NONE) {
+    if (p.pre != nullptr) st_v4(p.pre + row * p.n + col, pack_bf8(f));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = apply_act(f[i], p.act);
+  }
+  if (p.out_f32) {
+    float* y = static_cast<float*>(p.y) + row * p.n + col;
+    st_v4(y, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+    st_v4(y + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+  } else {
+    st_v4(static_cast<uint16_t*>(p.y) + row * p.n + col, pack_bf8(f));
+  }
+}
+
+}  // namespace tpx

@@ -1,0 +1,370 @@
+// Weight gradients over ragged segments: dW_e = sum over the rows i of segment e of x[row_i]^T dy_i.
+//
+// Here the ragged dimension is the contraction. CTA pairs (tcgen05 cta_group::2) compute 256 x 256 tiles
+// of dW_e, each CTA holding 128 of x's columns and 128 of dy's per 64-row k-block; both operands are
+// M-major as they lie in memory. Whole k-blocks come by TMA (x's rows four at a time by index when
+// they are gathered). A segment's last, partial k-block is loaded row by row and the rest of the
+// tile is set to zero in shared memory for both operands, so that a neighbour's rows (whatever they
+// hold) never enter.
+//
+// Tensor cores add each K=16 step to the accumulator with truncation: over a long contraction the
+// sum is short by about K / 32 times 2^-24 of itself (measured 4.4e-6 at K = 4096, 1.9e-5 at 16384).
+// A tile is therefore accumulated in spans of at most 512 rows, alternating between the two TMEM
+// accumulators; the epilogue warps add the spans in binary32, round-to-nearest, in registers (span
+// order, so results do not depend on timing). An empty segment writes zeros.
+#include <cstring>
+
+#include "ragged.cuh"
+#include "tmap.cuh"
+
+namespace tpx {
+namespace {
+
+constexpr int BK = 64;
+constexpr int KB = 2;                                // k-blocks per stage
+constexpr int STAGES = 3;
+constexpr uint32_t HALF = 128 * BK * 2;              // one k-block of one operand of this CTA: 16 KiB
+constexpr uint32_t BOX = 64 * BK * 2;                // 64 columns x 64 rows: 8 KiB
+constexpr uint32_t OP_STAGE = KB * HALF;             // 32 KiB
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int SPAN_KB = 8;                           // k-blocks per accumulator span (512 rows)
+constexpr int THREADS = 320;                         // loads, MMA, 8 epilogue warps
+constexpr uint32_t STG_WARP = 32 * 128;
+constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + 8 * STG_WARP + 256;
+
+struct DwParams {
+  CUtensorMap tx, tx_row;      // x [x_rows][k]: 64 x 64 boxes, and boxes one row high
+  CUtensorMap td, td_row;      // dy [R][n]
+  const int32_t* offsets;
+  const int32_t* row_index;
+  void* dw;
+  int R, x_rows, E, k, n, tiles_k, tiles_n, units;
+  bool out_f32;
+  uint32_t* status;
+  unsigned long long budget;
+};
+
+struct Dw {
+  uint8_t *sA, *sB;
+  uint32_t full0, empty0, accf0, acce0, drain, full0_leader, acce0_leader;
+  volatile uint32_t* abort_flag;
+  uint32_t rank;
+};
+
+__device__ __forceinline__ bool dw_fail(const DwParams& p, const Dw& c, uint32_t site) {
+  if (!*c.abort_flag) record_timeout(p.status, site);
+  *c.abort_flag = 1u;
+  return false;
+}
+
+// One 64-row k-block of one operand (this CTA's 128 columns from x0): rows r0 .. r0 + v - 1 of the
+// sorted order. Whole warp. Returns the bytes that the loads will count.
+__device__ __forceinline__ uint32_t load_operand(uint32_t dst, uint8_t* dst_ptr, const CUtensorMap* box,
+                                                 const CUtensorMap* row, const int32_t* index, int limit, int x0, int r0,
+                                                 int v, uint32_t fb, int lane) {
+  const int half = lane >> 4, grp = lane & 15;
+  if (v == BK && index == nullptr) {
+    if (lane < 2) tma_load_2d_pair(dst + lane * BOX, box, x0 + 64 * lane, r0, fb);
+    return 2 * BOX;
+  }
+  bool all_in = true;
+  int4 r = make_int4(0, 0, 0, 0);
+  if (index != nullptr && v == BK) {
+    const int i = r0 + 4 * grp;
+    r = make_int4(__ldg(index + i), __ldg(index + i + 1), __ldg(index + i + 2), __ldg(index + i + 3));
+    all_in = r.x >= 0 && r.x < limit && r.y >= 0 && r.y < limit && r.z >= 0 && r.z < limit && r.w >= 0 && r.w < limit;
+  }
+  all_in = __all_sync(0xffffffffu, all_in);
+  if (v == BK && all_in) {
+    tma_gather4_pair(dst + half * BOX + grp * 512u, row, x0 + 64 * half, r.x, r.y, r.z, r.w, fb);
+    return 2 * BOX;
+  }
+  // a partial k-block, or rows of x that do not exist: row by row, zeros elsewhere
+  uint32_t rows = 0;
+#pragma unroll
+  for (int j0 = 0; j0 < BK; j0 += 32) {
+    const int j = j0 + lane;
+    int at = -1;
+    if (j < v) {
+      at = index != nullptr ? __ldg(index + r0 + j) : r0 + j;
+      if (at < 0 || at >= limit) at = -1;
+    }
+    rows += __popc(__ballot_sync(0xffffffffu, at >= 0));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (at >= 0) {
+        tma_load_2d_pair(dst + h * BOX + j * 128u, row, x0 + 64 * h, at, fb);
+      } else {
+        uint4* line = reinterpret_cast<uint4*>(dst_ptr + h * BOX + j * 128);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) line[q] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  fence_proxy_async();
+  __syncwarp();
+  return rows * 256u;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    ragged_dw_kernel(const __grid_constant__ DwParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  Dw c;
+  c.sA = smem;
+  c.sB = smem + STAGES * OP_STAGE;
+  const uint32_t staging0 = smem_u32(smem + STAGES * 2 * OP_STAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * OP_STAGE + 8 * STG_WARP);
+  c.full0 = smem_u32(bars);
+  c.empty0 = c.full0 + 8 * STAGES;
+  c.accf0 = c.empty0 + 8 * STAGES;
+  c.acce0 = c.accf0 + 16;
+  c.drain = c.acce0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  c.abort_flag = tmem_slot + 1;
+  c.rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.tx);
+    prefetch_tmap(&p.tx_row);
+    prefetch_tmap(&p.td);
+    prefetch_tmap(&p.td_row);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(c.full0 + 8 * s, 2);            // both CTAs' producers, on the leader's barrier
+      mbar_init(c.empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(c.accf0 + 8 * a, 1);
+      mbar_init(c.acce0 + 8 * a, 16);           // epilogue warps of both CTAs
+    }
+    mbar_init(c.drain, 1);
+    *c.abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  c.full0_leader = mapa_shared(c.full0, 0);
+  c.acce0_leader = mapa_shared(c.acce0, 0);
+  const uint32_t tmem_base = *tmem_slot;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int per_seg = p.tiles_k * p.tiles_n;
+  bool mma_issued = false;
+  int loaded = 0;                               // warp 0: stages filled
+
+  if (warp == 0) {
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < p.units; u += pairs) {
+      const int e = u / per_seg, local = u - e * per_seg;
+      const int a0 = (local % p.tiles_k) * 256 + static_cast<int>(c.rank) * 128;
+      const int b0 = (local / p.tiles_k) * 256 + static_cast<int>(c.rank) * 128;
+      const int begin = seg_bound(p.offsets, e, p.R), end = seg_bound(p.offsets, e + 1, p.R);
+      for (int r = begin; r < end; r += KB * BK) {
+        ok = mbar_wait_bounded(c.empty0 + 8 * st, phase ^ 1u, p.budget, c.abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          dw_fail(p, c, WAIT_PRODUCER_EMPTY);
+          break;
+        }
+        const uint32_t fb = c.full0_leader + 8 * st;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int h = 0; h < KB; ++h) {
+          const int r0 = r + h * BK, v = min(BK, end - r0);
+          if (v <= 0) break;                    // not multiplied either
+          const uint32_t off = st * OP_STAGE + h * HALF;
+          bytes += load_operand(smem_u32(c.sA + off), c.sA + off, &p.tx, &p.tx_row, p.row_index, p.x_rows, a0, r0, v, fb, lane);
+          bytes += load_operand(smem_u32(c.sB + off), c.sB + off, &p.td, &p.td_row, nullptr, p.R, b0, r0, v, fb, lane);
+        }
+        if (lane == 0) mbar_arrive_expect_tx_cluster(fb, bytes);
+        ++loaded;
+        if (++st == STAGES) { st = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && c.rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, 256, true, true);
+      int st = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.units; u += pairs) {
+        const int e = u / per_seg;
+        const int rows = seg_bound(p.offsets, e + 1, p.R) - seg_bound(p.offsets, e, p.R);
+        const int num_kb = rows > 0 ? (rows + BK - 1) / BK : 0;
+        for (int kb = 0; ok && kb < num_kb; kb += KB) {
+          const int in_span = kb % SPAN_KB;
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
+          if (in_span == 0) {
+            bool got = mbar_try_wait_cluster(c.acce0 + 8 * acc, acc_phase ^ 1u);
+            const long long t0 = clock64();
+            while (!got && !*c.abort_flag && static_cast<unsigned long long>(clock64() - t0) <= p.budget)
+              got = mbar_try_wait_cluster(c.acce0 + 8 * acc, acc_phase ^ 1u);
+            if (!got) { ok = dw_fail(p, c, WAIT_MMA_ACC_EMPTY); break; }
+            tc_fence_after();
+          }
+          {
+            bool got = mbar_try_wait_cluster(c.full0 + 8 * st, phase);
+            const long long t0 = clock64();
+            while (!got && !*c.abort_flag && static_cast<unsigned long long>(clock64() - t0) <= p.budget)
+              got = mbar_try_wait_cluster(c.full0 + 8 * st, phase);
+            if (!got) { ok = dw_fail(p, c, WAIT_MMA_FULL); break; }
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < KB; ++h) {
+            if (kb + h < num_kb) {
+              const uint32_t a = smem_u32(c.sA + st * OP_STAGE + h * HALF);
+              const uint32_t b = smem_u32(c.sB + st * OP_STAGE + h * HALF);
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                umma_bf16_pair(d, smem_desc_sw128(a + 2048u * k, BOX, 1024u), smem_desc_sw128(b + 2048u * k, BOX, 1024u),
+                               idesc, (in_span + h) != 0 || k != 0 ? 1u : 0u);
+            }
+          }
+          mma_issued = true;
+          umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
+          if (in_span + KB >= SPAN_KB || kb + KB >= num_kb) {
+            umma_commit_pair_mc(c.accf0 + 8 * acc, 0x3);
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+          }
+        }
+      }
+    }
+  } else {
+    // warps 2..9: TMEM lane quadrant = warp % 4 (rows of dW); warps 2..5 the left 128 columns, 6..9
+    // the right. Each thread holds the running sums of one row's 128 columns.
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t stg = staging0 + static_cast<uint32_t>(warp - 2) * STG_WARP;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    float sum[4][32];
+    for (int u = pair; ok && u < p.units; u += pairs) {
+      const int e = u / per_seg, local = u - e * per_seg;
+      const int row0 = (local % p.tiles_k) * 256 + static_cast<int>(c.rank) * 128 + quad * 32;
+      const int col0 = (local / p.tiles_k) * 256 + half * 128;
+      const int rows = seg_bound(p.offsets, e + 1, p.R) - seg_bound(p.offsets, e, p.R);
+      const int spans = rows > 0 ? (rows + SPAN_KB * BK - 1) / (SPAN_KB * BK) : 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[q][i] = 0.0f;
+      for (int s = 0; s < spans; ++s) {
+        if (!mbar_wait_bounded(c.accf0 + 8 * acc, acc_phase, p.budget, c.abort_flag)) {
+          ok = dw_fail(p, c, WAIT_EPI_ACC_FULL);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(t + q * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[q][i] = __fadd_rn(sum[q][i], __uint_as_float(v[i]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(c.acce0_leader + 8 * acc);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      if (!ok) break;
+      // one row a lane -> whole 128-byte row pieces, through this warp's staging buffer
+      const int sub = lane & 7;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                       "f"(sum[q][4 * j]), "f"(sum[q][4 * j + 1]), "f"(sum[q][4 * j + 2]), "f"(sum[q][4 * j + 3])
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 4 * j + (lane >> 3);
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(stg + r * 128 + ((sub ^ (r & 7)) << 4))
+                       : "memory");
+          const int row = row0 + r, col = col0 + q * 32 + 4 * sub;
+          if (row < p.k && col < p.n) {
+            const int64_t at = (static_cast<int64_t>(e) * p.k + row) * p.n + col;
+            if (p.out_f32)
+              st_v4(static_cast<float*>(p.dw) + at,
+                    make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)));
+            else
+              st_v2(static_cast<uint16_t*>(p.dw) + at, make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w)));
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // all pair MMAs done, then both CTAs meet before either frees TMEM or exits. After a wait that ran
+  // out, the copies still in flight land first (they count on the leader's barriers).
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*c.abort_flag != 0u && warp == 0 && lane == 0 && c.rank == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      const int uses = (loaded - s + STAGES - 1) / STAGES;
+      if (uses > 0 && !mbar_wait_bounded(c.full0 + 8 * s, (uses - 1) & 1, 400000000ull, nullptr))
+        record_timeout(p.status, WAIT_TEARDOWN);
+    }
+  }
+  if (warp == 1 && lane == 0 && c.rank == 0 && mma_issued) {
+    umma_commit_pair(c.drain);
+    if (!mbar_wait_bounded(c.drain, 0, 4000000000ull, nullptr)) record_timeout(p.status, WAIT_TEARDOWN);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+}  // namespace
+
+tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
+  DwParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.offsets = g.offsets; p.row_index = g.row_index; p.dw = g.dw;
+  p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
+  p.E = g.E; p.k = static_cast<int>(g.k); p.n = static_cast<int>(g.n);
+  p.tiles_k = (p.k + 255) / 256;
+  p.tiles_n = (p.n + 255) / 256;
+  const int64_t units = static_cast<int64_t>(g.E) * p.tiles_k * p.tiles_n;
+  if (units > INT32_MAX / 2) return fail(TP_ESHAPE, "too many tiles");
+  p.units = static_cast<int>(units);
+  p.out_f32 = g.out_f32;
+  if (!encode_bf16_2d(&p.tx, g.x, g.k, g.x_rows, g.k, 64, 64) || !encode_bf16_2d(&p.tx_row, g.x, g.k, g.x_rows, g.k, 64, 1) ||
+      !encode_bf16_2d(&p.td, g.dy, g.n, g.R, g.n, 64, 64) || !encode_bf16_2d(&p.td_row, g.dy, g.n, g.R, g.n, 64, 1))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptors");
+  p.status = status_word();
+  p.budget = wait_budget();
+  if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");
+  static int configured_for[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
+  if (dev < 0 || dev >= 64 || !configured_for[dev]) {
+    if (cudaFuncSetAttribute(ragged_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM)) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
+    if (dev >= 0 && dev < 64) configured_for[dev] = 1;
+  }
+  const int sms = sm_count();
+  int grid = 2 * units < sms ? static_cast<int>(2 * units) : (sms & ~1);
+  if (grid < 2) grid = 2;
+  ragged_dw_kernel<<<grid, THREADS, SMEM, s>>>(p);
+  return check_launch("ragged_dw_kernel");
+}
+
+}  // namespace tpx
