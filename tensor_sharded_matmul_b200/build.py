@@ -24,7 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtp.so")
 
 SOURCES = ["status.cu", "layouts.cu", "collectives.cu", "gemm.cu", "api.cu", "backward.cu", "noalloc.cu", "ragged.cu",
-           "ragged_dw.cu", "moe.cu"]
+           "ragged_pair.cu", "ragged_dw.cu", "moe.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -186,18 +186,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
             const int r0 = (c % per_adapter) * 16 + sub * 8;
             const int i = i0 + row;
             if (i >= s_off[a] && i < s_off[a + 1] && r0 < p.rank) {
-              const float4* src = reinterpret_cast<const float4*>(p.v + static_cast<int64_t>(i) * p.rank + r0);
-              const float4 f0 = src[0], f1 = src[1];
-              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-              float h[8], l[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                h[q] = bf(to_bf(f[q]));
-                l[q] = f[q] - h[q];
-                if (!(fabsf(l[q]) < 1e38f)) l[q] = 0.0f;   // infinite or NaN v: hi alone carries it
-              }
-              hi = pack_bf8(h);
-              lo = pack_bf8(l);
+              split_bf8(p.v + static_cast<int64_t>(i) * p.rank + r0, hi, lo);
             }
           }
           uint8_t* line = s_x + st * X_STAGE + row * 128;
@@ -382,9 +371,11 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the up half of the weights");
   if (!encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
+  if (!encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 32))
+    return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
-  p.offsets = g.offsets; p.row_index = g.row_index; p.seg_scale = g.seg_scale;
+  p.x = g.x; p.offsets = g.offsets; p.row_index = g.row_index; p.seg_scale = g.seg_scale;
   p.y = g.y; p.pre = g.pre; p.h_pre = g.h_pre; p.v = g.v;
   p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
   p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
@@ -398,6 +389,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   p.tiles_n = static_cast<int>((g.n + tile_n - 1) / tile_n);
   const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
   const bool narrow = g.R <= 64 * segs;
+  if (!narrow) return ragged_pairs(p, swiglu, lora, lora ? (g.R + 255) / 256 : g.R / 256 + segs, s);
   const int nt = narrow ? 64 : 256;
   const int64_t row_tiles = lora ? (g.R + nt - 1) / nt : g.R / nt + segs;
   const int64_t units = row_tiles * p.tiles_n * (lora ? g.E : 1);

@@ -20,9 +20,11 @@ struct RaggedParams {
   CUtensorMap tw;             // W: [E][K][n], or [E][n][K] (w_km); the gate half for SwiGLU
   CUtensorMap tw2;            // SwiGLU: the up half
   CUtensorMap tx;             // x: [x_rows][K], boxes one row high (gathered rows)
+  CUtensorMap tx_box;         // x: boxes of 32 rows (rows side by side)
   CUtensorMap tb;             // adapters: B [t * L][rank][n]
   const int32_t* offsets;     // [E + 1]; adapters: [L + 1], the segments of the adapters
   const int32_t* row_index;   // x's row of sorted row i; nullptr: i
+  const uint16_t* x;
   const float* seg_scale;     // optional factor of every row of segment e
   void* y;                    // output rows, stride n
   uint16_t* pre;              // optional: the products before the activation (SwiGLU: [gate | up], stride 2n)
@@ -64,6 +66,8 @@ struct RaggedArgs {
   int L, rank;
 };
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
+// The same on CTA pairs (row_tiles: how many tiles of 256 rows there can be).
+tp_status ragged_pairs(RaggedParams& p, bool swiglu, bool lora, int64_t row_tiles, cudaStream_t s);
 
 // Host-side arguments of ragged_dw: dw[e] = x_e^T dy_e for every segment.
 struct RaggedDwArgs {
@@ -132,6 +136,22 @@ __device__ __forceinline__ void unpack_bf8(uint4 v, float (&f)[8]) {
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+
+// Eight binary32 numbers as bf16 pairs, v = hi + lo with |v - hi - lo| <= 2^-16 |v|. An infinite or NaN
+// v is carried by hi alone.
+__device__ __forceinline__ void split_bf8(const float* v, uint4& hi, uint4& lo) {
+  const float4 a = *reinterpret_cast<const float4*>(v), b = *reinterpret_cast<const float4*>(v + 4);
+  const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float h[8], l[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    h[q] = bf(to_bf(f[q]));
+    l[q] = f[q] - h[q];
+    if (!(fabsf(l[q]) < 1e38f)) l[q] = 0.0f;
+  }
+  hi = pack_bf8(h);
+  lo = pack_bf8(l);
 }
 
 __device__ __forceinline__ float apply_act(float x, int act) {

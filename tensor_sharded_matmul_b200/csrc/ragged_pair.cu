@@ -1,0 +1,470 @@
+// The ragged products of ragged.cu for segments of many rows: CTA pairs, persistent.
+//
+// The same transposed product, D^T = W_e^T x^T, on tcgen05 cta_group::2: 256 columns of W are the M
+// of a pair (128 per CTA; SwiGLU: 64 gate and 64 up columns per CTA), and up to 256 rows of a segment
+// its N, in steps of 32, each CTA holding half of them. A segment of r rows is cut into ceil(r / 256)
+// tiles of nearly equal height, so that its last tile is not a sliver that streams all of W for a few rows.
+//
+// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 6..9 fetch gathered rows
+// with 16-byte cp.async into the swizzled layout (tile::gather4 moved one 128-byte row in about 19
+// cycles here, which bound the first version of this kernel at 221 TFLOP/s; zero rows for indices
+// outside x come from cp.async's zero fill); one thread of the leader's warp 1 issues the MMAs; warps
+// 2..5 turn each 32 rows of the accumulator around through shared memory and write whole row pieces
+// while the next tile is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
+//
+// A wait that runs out is agreed on by the four epilogue warps before any of them leaves, since they meet
+// at a named barrier.
+#include <cstring>
+
+#include "ragged.cuh"
+#include "tmap.cuh"
+
+namespace tpx {
+namespace {
+
+constexpr int BK = 64;
+constexpr int KB = 2;                               // k-blocks per stage
+constexpr int STAGES = 3;
+constexpr int NT = 256;                             // rows of a tile, at most
+constexpr uint32_t HALF = 128 * BK * 2;             // one k-block of one operand of this CTA: 16 KiB
+constexpr uint32_t BOX = 64 * BK * 2;               // 64 columns x 64 k: 8 KiB
+constexpr uint32_t OP_STAGE = KB * HALF;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int THREADS = 320;
+constexpr int STG_LD = 128 + 4;                     // floats between staged rows
+constexpr uint32_t STAGING = 32 * STG_LD * 4;
+constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + STAGING + 256 + (TP_MAX_EXPERTS + 4) * 4;
+constexpr unsigned long long DRAIN = 400000000ull;
+
+struct Pair {
+  uint8_t *sW, *sX;
+  uint32_t full0, empty0, accf0, acce0, drain, full0_leader, acce0_leader;
+  volatile uint32_t* abort_flag;
+  uint32_t rank;
+};
+
+__device__ __forceinline__ bool pair_fail(const RaggedParams& p, const Pair& c, uint32_t site) {
+  if (!*c.abort_flag) record_timeout(p.status, site);
+  *c.abort_flag = 1u;
+  return false;
+}
+
+// Bounded wait of a whole warp on a barrier that the other CTA may arrive on; all lanes agree.
+__device__ __forceinline__ bool warp_wait(const RaggedParams& p, const Pair& c, uint32_t bar, uint32_t parity, uint32_t site) {
+  bool got = mbar_try_wait_cluster(bar, parity);
+  if (!__all_sync(0xffffffffu, got)) {
+    const long long t0 = clock64();
+    while (!got && !*c.abort_flag && static_cast<unsigned long long>(clock64() - t0) <= p.budget)
+      got = mbar_try_wait_cluster(bar, parity);
+    got = __all_sync(0xffffffffu, got);
+  }
+  return got ? true : pair_fail(p, c, site);
+}
+
+struct Tile {
+  int e, i0, valid, n_mma, n0;
+  bool live;
+};
+
+// Tile u. Token tiles of a segment are neighbours, so that the running pairs share W's columns.
+template <bool SWIGLU, bool LORA>
+__device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off, int u, int lane) {
+  Tile t;
+  int rows, count, rt, ct, first;
+  if (LORA) {
+    rows = p.R;
+    first = 0;
+    count = (rows + NT - 1) / NT;
+    rt = u % count;
+    ct = u / count;
+    t.e = ct / p.tiles_n;
+    ct -= t.e * p.tiles_n;
+    t.live = t.e < p.E;
+  } else {
+    const SegTile s = find_seg_tile<NT>(off, p.E, u / p.tiles_n, lane);
+    t.live = s.live;
+    t.e = s.e;
+    first = off[s.e];
+    rows = off[s.e + 1] - first;
+    count = max(s.count, 1);
+    const int local = u - s.before * p.tiles_n;
+    rt = local % count;
+    ct = local / count;
+  }
+  const int step = ((rows + count - 1) / count + 31) & ~31;
+  t.i0 = first + rt * step;
+  t.valid = min(step, rows - rt * step);
+  t.n_mma = (t.valid + 31) & ~31;
+  t.n0 = ct * (SWIGLU ? 128 : 256);
+  return t;
+}
+
+// Adapters that own rows of [i0, i0 + valid): how many, and the first from `a` on.
+__device__ __forceinline__ int count_adapters(const int* off, int L, int i0, int valid, int lane) {
+  int n = 0;
+  for (int a0 = 0; a0 < L; a0 += 32) {
+    const int a = a0 + lane;
+    const bool in = a < L && max(off[a], i0) < min(off[a + 1], i0 + valid);
+    n += __popc(__ballot_sync(0xffffffffu, in));
+  }
+  return n;
+}
+__device__ __forceinline__ int next_adapter(const int* off, int L, int i0, int valid, int a) {
+  while (a < L && !(max(off[a], i0) < min(off[a + 1], i0 + valid))) ++a;
+  return a;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <bool SWIGLU, bool LORA>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    ragged_pair_kernel(const __grid_constant__ RaggedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  Pair c;
+  c.sW = smem;
+  c.sX = smem + STAGES * OP_STAGE;
+  float* staging = reinterpret_cast<float*>(smem + STAGES * 2 * OP_STAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * OP_STAGE + STAGING);
+  c.full0 = smem_u32(bars);
+  c.empty0 = c.full0 + 8 * STAGES;
+  c.accf0 = c.empty0 + 8 * STAGES;
+  c.acce0 = c.accf0 + 16;
+  c.drain = c.acce0 + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  c.abort_flag = tmem_slot + 1;
+  int* s_off = reinterpret_cast<int*>(bars + 32);
+  c.rank = cluster_ctarank();
+  const bool gather = LORA || p.row_index != nullptr;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.tw);
+    if (SWIGLU) prefetch_tmap(&p.tw2);
+    if (LORA) prefetch_tmap(&p.tb);
+    if (!gather) prefetch_tmap(&p.tx_box);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(c.full0 + 8 * s, gather ? 10 : 2);   // both CTAs' TMA warps, and their four row loaders
+      mbar_init(c.empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(c.accf0 + 8 * a, 1);
+      mbar_init(c.acce0 + 8 * a, 8);                 // epilogue warps of both CTAs
+    }
+    mbar_init(c.drain, 1);
+    *c.abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  const int segs = LORA ? p.L : p.E;
+  for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  c.full0_leader = mapa_shared(c.full0, 0);
+  c.acce0_leader = mapa_shared(c.acce0, 0);
+  const uint32_t tmem_base = *tmem_slot;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int per_adapter = LORA ? (p.rank + 15) / 16 : 1;
+  bool mma_issued = false;
+  int loaded = 0;                                    // warp 0: stages begun
+
+  if (warp == 0) {
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok; u += pairs) {
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      if (!t.live) break;
+      const int col = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
+      const int nh = t.n_mma / 2, row0 = t.i0 + static_cast<int>(c.rank) * nh;
+      const int boxes = gather ? 0 : (nh + 31) / 32;
+      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+      const int total_kb = p.num_kb + (chunks + 1) / 2;
+      int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
+      for (int kb = 0; kb < total_kb; kb += KB) {
+        ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t fb = c.full0_leader + 8 * st;
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int h = 0; h < KB; ++h) {
+            if (kb + h < p.num_kb) bytes += HALF + boxes * 4096u;
+            else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 4096u;
+          }
+          mbar_arrive_expect_tx_cluster(fb, bytes);
+#pragma unroll
+          for (int h = 0; h < KB; ++h) {
+            const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
+            if (kb + h < p.num_kb) {
+              const int k0 = (kb + h) * BK;
+              if (p.w_km) {
+                tma_load_3d_pair(w, &p.tw, k0, col, t.e, fb);
+              } else {
+                tma_load_3d_pair(w, &p.tw, col, k0, t.e, fb);
+                tma_load_3d_pair(w + BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? col : col + 64, k0, t.e, fb);
+              }
+              for (int b = 0; b < boxes; ++b) tma_load_2d_pair(x + 4096u * b, &p.tx_box, k0, row0 + 32 * b, fb);
+            } else if (LORA && kb + h < total_kb) {
+              const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
+              for (int ch = 0; ch < nch; ++ch) {
+                tma_load_3d_pair(w + ch * 2048u, &p.tb, col, q * 16, t.e * p.L + a, fb);
+                tma_load_3d_pair(w + ch * 2048u + BOX, &p.tb, col + 64, q * 16, t.e * p.L + a, fb);
+                if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        ++loaded;
+        if (++st == STAGES) { st = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    if (c.rank == 0) {
+      int st = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok; u += pairs) {
+        const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+        if (!t.live) break;
+        const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+        const int total_kb = p.num_kb + (chunks + 1) / 2;
+        const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !p.w_km, false);
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
+        ok = warp_wait(p, c, c.acce0 + 8 * acc, acc_phase ^ 1u, WAIT_MMA_ACC_EMPTY);
+        if (!ok) break;
+        tc_fence_after();
+        for (int kb = 0; kb < total_kb; kb += KB) {
+          ok = warp_wait(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < KB; ++h) {
+              const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
+              if (kb + h < p.num_kb) {
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k) {
+                  const uint64_t ad = p.w_km ? smem_desc_sw128(w + 32u * k, 16u, 1024u) : smem_desc_sw128(w + 2048u * k, BOX, 1024u);
+                  umma_bf16_pair(d, ad, smem_desc_sw128(x + 32u * k, 16u, 1024u), idesc, (kb + h) != 0 || k != 0 ? 1u : 0u);
+                }
+              } else if (LORA && kb + h < total_kb) {
+                const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
+                for (int i = 0; i < 2 * nch; ++i) {   // hi and lo of each step against the same rows of B
+                  const int ch = i >> 1, half = i & 1;
+                  umma_bf16_pair(d, smem_desc_sw128(w + 2048u * ch, BOX, 1024u),
+                                 smem_desc_sw128(x + 32u * (ch + 2 * half), 16u, 1024u), idesc, 1u);
+                }
+              }
+            }
+            umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
+            if (kb + KB >= total_kb) umma_commit_pair_mc(c.accf0 + 8 * acc, 0x3);
+          }
+          __syncwarp();
+          mma_issued = true;
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
+        }
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+    }
+  } else if (warp < 6) {
+    const int quad = warp & 3;
+    const int tid = threadIdx.x - 64;
+    constexpr int GROUPS = SWIGLU ? 8 : 16;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int u = pair;; u += pairs) {
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      if (!t.live) break;
+      const int col0 = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
+      int got = warp_wait(p, c, c.accf0 + 8 * acc, acc_phase, WAIT_EPI_ACC_FULL) ? 1 : 0;
+      // all four warps go on, or none
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.s32 p, %0, 0;\n\t"
+          "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+          "selp.s32 %0, 1, 0, q;\n\t}\n"
+          : "+r"(got)::"memory");
+      if (!got) break;
+      tc_fence_after();
+      const uint32_t tm = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      for (int j0 = 0; j0 < t.valid; j0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(tm + j0, v);
+        tmem_ld_wait();
+        if (j0 + 32 >= t.valid) {                     // the accumulator is read: the next tile may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(c.acce0_leader + 8 * acc);
+        }
+        float* s = staging + quad * 32 + lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[j * STG_LD] = __uint_as_float(v[j]);
+        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+        const int items = min(32, t.valid - j0) * GROUPS;
+        for (int it = tid; it < items; it += 128) {
+          const int j = it / GROUPS, c8 = (it % GROUPS) * 8;
+          const int col = col0 + c8;
+          if (col >= p.n) continue;
+          float f[8], up[8];
+          const float4* src = reinterpret_cast<const float4*>(staging + j * STG_LD + c8);
+          *reinterpret_cast<float4*>(f) = src[0];
+          *reinterpret_cast<float4*>(f + 4) = src[1];
+          if constexpr (SWIGLU) {
+            *reinterpret_cast<float4*>(up) = src[16];
+            *reinterpret_cast<float4*>(up + 4) = src[17];
+          }
+          const int i = t.i0 + j0 + j;
+          if (p.seg_scale != nullptr) {
+            const float sc = __ldg(p.seg_scale + t.e);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] *= sc;
+          }
+          if constexpr (LORA) {
+            const int r = __ldg(p.row_index + i);
+            if (r >= 0 && r < p.x_rows) store_row8(p, static_cast<int64_t>(t.e) * p.R + r, col, f, up);
+          } else {
+            store_row8(p, i, col, f, up);
+          }
+        }
+        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+  } else if (gather) {
+    // Row loaders: eight lanes fetch one row's 128 bytes of a k-block; a stage is handed over when its
+    // copies have landed, one stage after they were issued.
+    const int tid = threadIdx.x - 192;
+    const int piece = tid & 7, r0 = tid >> 3;
+    int st = 0, pending = -1;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok; u += pairs) {
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      if (!t.live) break;
+      const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
+      const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
+      int idx[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = r0 + 16 * i;
+        idx[i] = -2;                                   // no row: left as it is (its column is not read)
+        if (row < mine) {
+          const int r = __ldg(p.row_index + t.i0 + half0 + row);
+          idx[i] = r >= 0 && r < p.x_rows ? r : -1;    // -1: outside x, zeros
+        }
+      }
+      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+      const int total_kb = p.num_kb + (chunks + 1) / 2;
+      int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
+      for (int kb = 0; kb < total_kb; kb += KB) {
+        ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < KB; ++h) {
+          uint8_t* x = c.sX + st * OP_STAGE + h * HALF;
+          if (kb + h < p.num_kb) {
+            const int k = (kb + h) * BK + piece * 8;
+            const bool in_k = k < p.K;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = r0 + 16 * i;
+              if (idx[i] != -2) {
+                const bool fetch = in_k && idx[i] >= 0;
+                const uint16_t* src = fetch ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x;
+                cp_async16(smem_u32(x) + row * 128 + ((piece ^ (row & 7)) << 4), src, fetch ? 16u : 0u);
+              }
+            }
+          } else if (LORA && kb + h < total_kb) {
+            const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
+            for (int ch = 0; ch < nch; ++ch) {
+              for (int it = tid; it < 2 * nh; it += 128) {
+                const int row = it >> 1, sub = it & 1;
+                const int i = t.i0 + half0 + row, k0 = q * 16 + sub * 8;
+                uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+                if (row < mine && i >= s_off[a] && i < s_off[a + 1] && k0 < p.rank)
+                  split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k0, hi, lo);
+                uint8_t* line = x + row * 128;
+                const int pc = 2 * ch + sub;
+                *reinterpret_cast<uint4*>(line + ((pc ^ (row & 7)) << 4)) = hi;
+                *reinterpret_cast<uint4*>(line + (((pc + 4) ^ (row & 7)) << 4)) = lo;
+              }
+              if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+            }
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (pending >= 0) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(c.full0_leader + 8 * pending);
+        }
+        pending = st;
+        if (++st == STAGES) { st = 0; phase ^= 1u; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok && pending >= 0) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(c.full0_leader + 8 * pending);
+    }
+  }
+  // all pair MMAs done, then both CTAs meet before either frees TMEM or exits. After a wait that ran
+  // out, the copies still in flight land first (they count on the leader's barriers).
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*c.abort_flag != 0u && warp == 0 && lane == 0 && c.rank == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      const int uses = (loaded - s + STAGES - 1) / STAGES;
+      if (uses > 0 && !mbar_wait_bounded(c.full0 + 8 * s, (uses - 1) & 1, DRAIN, nullptr)) record_timeout(p.status, WAIT_TEARDOWN);
+    }
+  }
+  if (warp == 1 && lane == 0 && c.rank == 0 && mma_issued) {
+    umma_commit_pair(c.drain);
+    if (!mbar_wait_bounded(c.drain, 0, 4000000000ull, nullptr)) record_timeout(p.status, WAIT_TEARDOWN);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+template <bool SWIGLU, bool LORA>
+tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
+  static int configured_for[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
+  if (dev < 0 || dev >= 64 || !configured_for[dev]) {
+    if (cudaFuncSetAttribute(ragged_pair_kernel<SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SMEM)) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
+    if (dev >= 0 && dev < 64) configured_for[dev] = 1;
+  }
+  const int sms = sm_count();
+  int grid = 2 * units < sms ? static_cast<int>(2 * units) : (sms & ~1);
+  if (grid < 2) grid = 2;
+  ragged_pair_kernel<SWIGLU, LORA><<<grid, THREADS, SMEM, s>>>(p);
+  return check_launch("ragged_pair_kernel");
+}
+
+}  // namespace
+
+tp_status ragged_pairs(RaggedParams& p, bool swiglu, bool lora, int64_t row_tiles, cudaStream_t s) {
+  p.tiles_n = (p.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+  const int64_t units = row_tiles * p.tiles_n * (lora ? p.E : 1);
+  if (units > INT32_MAX / 2) return fail(TP_ESHAPE, "too many tiles");
+  if (lora) return launch_pair<false, true>(p, units, s);
+  return swiglu ? launch_pair<true, false>(p, units, s) : launch_pair<false, false>(p, units, s);
+}
+
+}  // namespace tpx
