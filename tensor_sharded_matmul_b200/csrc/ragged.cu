@@ -371,7 +371,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the up half of the weights");
   if (!encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
-  if (!encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 32))
+  if (!encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128) || !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, 32))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");

@@ -20,7 +20,8 @@ struct RaggedParams {
   CUtensorMap tw;             // W: [E][K][n], or [E][n][K] (w_km); the gate half for SwiGLU
   CUtensorMap tw2;            // SwiGLU: the up half
   CUtensorMap tx;             // x: [x_rows][K], boxes one row high (gathered rows)
-  CUtensorMap tx_box;         // x: boxes of 32 rows (rows side by side)
+  CUtensorMap tx_box;         // x: boxes of 128 rows (rows side by side)
+  CUtensorMap tx_box32;       // x: boxes of 32 rows
   CUtensorMap tb;             // adapters: B [t * L][rank][n]
   const int32_t* offsets;     // [E + 1]; adapters: [L + 1], the segments of the adapters
   const int32_t* row_index;   // x's row of sorted row i; nullptr: i

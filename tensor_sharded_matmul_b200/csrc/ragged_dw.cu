@@ -3,9 +3,9 @@
 // Here the ragged dimension is the contraction. CTA pairs (tcgen05 cta_group::2) compute 256 x 256 tiles
 // of dW_e, each CTA holding 128 of x's columns and 128 of dy's per 64-row k-block; both operands are
 // M-major as they lie in memory. Whole k-blocks come by TMA (x's rows four at a time by index when
-// they are gathered). A segment's last, partial k-block is loaded row by row and the rest of the
-// tile is set to zero in shared memory for both operands, so that a neighbour's rows (whatever they
-// hold) never enter.
+// they are gathered). A segment's last, partial k-block is loaded row by row, and the rest of the tile from
+// rows past the end of the matrix, which TMA reads as zeros: in both operands, so that a
+// neighbour's rows (whatever they hold) never enter.
 //
 // Tensor cores add each K=16 step to the accumulator with truncation: over a long contraction the
 // sum is short by about K / 32 times 2^-24 of itself (measured 4.4e-6 at K = 4096, 1.9e-5 at 16384).
@@ -58,14 +58,14 @@ __device__ __forceinline__ bool dw_fail(const DwParams& p, const Dw& c, uint32_t
 }
 
 // One 64-row k-block of one operand (this CTA's 128 columns from x0): rows r0 .. r0 + v - 1 of the
-// sorted order. Whole warp. Returns the bytes that the loads will count.
-__device__ __forceinline__ uint32_t load_operand(uint32_t dst, uint8_t* dst_ptr, const CUtensorMap* box,
-                                                 const CUtensorMap* row, const int32_t* index, int limit, int x0, int r0,
-                                                 int v, uint32_t fb, int lane) {
+// sorted order, and zeros for the other rows of the tile and for indices outside 0 .. limit - 1 (a row past
+// the matrix reads as zeros). Whole warp; always counts 16 KiB.
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row,
+                                             const int32_t* index, int limit, int x0, int r0, int v, uint32_t fb, int lane) {
   const int half = lane >> 4, grp = lane & 15;
   if (v == BK && index == nullptr) {
     if (lane < 2) tma_load_2d_pair(dst + lane * BOX, box, x0 + 64 * lane, r0, fb);
-    return 2 * BOX;
+    return;
   }
   bool all_in = true;
   int4 r = make_int4(0, 0, 0, 0);
@@ -77,33 +77,19 @@ __device__ __forceinline__ uint32_t load_operand(uint32_t dst, uint8_t* dst_ptr,
   all_in = __all_sync(0xffffffffu, all_in);
   if (v == BK && all_in) {
     tma_gather4_pair(dst + half * BOX + grp * 512u, row, x0 + 64 * half, r.x, r.y, r.z, r.w, fb);
-    return 2 * BOX;
+    return;
   }
-  // a partial k-block, or rows of x that do not exist: row by row, zeros elsewhere
-  uint32_t rows = 0;
 #pragma unroll
   for (int j0 = 0; j0 < BK; j0 += 32) {
     const int j = j0 + lane;
-    int at = -1;
+    int at = limit;
     if (j < v) {
       at = index != nullptr ? __ldg(index + r0 + j) : r0 + j;
-      if (at < 0 || at >= limit) at = -1;
+      if (at < 0 || at > limit) at = limit;
     }
-    rows += __popc(__ballot_sync(0xffffffffu, at >= 0));
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (at >= 0) {
-        tma_load_2d_pair(dst + h * BOX + j * 128u, row, x0 + 64 * h, at, fb);
-      } else {
-        uint4* line = reinterpret_cast<uint4*>(dst_ptr + h * BOX + j * 128);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) line[q] = make_uint4(0, 0, 0, 0);
-      }
-    }
+    tma_load_2d_pair(dst + j * 128u, row, x0, at, fb);
+    tma_load_2d_pair(dst + BOX + j * 128u, row, x0 + 64, at, fb);
   }
-  fence_proxy_async();
-  __syncwarp();
-  return rows * 256u;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -131,7 +117,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefetch_tmap(&p.td);
     prefetch_tmap(&p.td_row);
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(c.full0 + 8 * s, 2);            // both CTAs' producers, on the leader's barrier
+      mbar_init(c.full0 + 8 * s, 1);
       mbar_init(c.empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -174,16 +160,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t fb = c.full0_leader + 8 * st;
-        uint32_t bytes = 0;
+        if (lane == 0 && c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, end - r > BK ? 8 * HALF : 4 * HALF);   // of both CTAs
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < KB; ++h) {
           const int r0 = r + h * BK, v = min(BK, end - r0);
           if (v <= 0) break;                    // not multiplied either
           const uint32_t off = st * OP_STAGE + h * HALF;
-          bytes += load_operand(smem_u32(c.sA + off), c.sA + off, &p.tx, &p.tx_row, p.row_index, p.x_rows, a0, r0, v, fb, lane);
-          bytes += load_operand(smem_u32(c.sB + off), c.sB + off, &p.td, &p.td_row, nullptr, p.R, b0, r0, v, fb, lane);
+          load_operand(smem_u32(c.sA + off), &p.tx, &p.tx_row, p.row_index, p.x_rows, a0, r0, v, fb, lane);
+          load_operand(smem_u32(c.sB + off), &p.td, &p.td_row, nullptr, p.R, b0, r0, v, fb, lane);
         }
-        if (lane == 0) mbar_arrive_expect_tx_cluster(fb, bytes);
         ++loaded;
         if (++st == STAGES) { st = 0; phase ^= 1u; }
       }

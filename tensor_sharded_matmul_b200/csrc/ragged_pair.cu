@@ -5,12 +5,18 @@
 // its N, in steps of 32, each CTA holding half of them. A segment of r rows is cut into ceil(r / 256)
 // tiles of nearly equal height, so that its last tile is not a sliver that streams all of W for a few rows.
 //
-// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 6..9 fetch gathered rows
-// with 16-byte cp.async into the swizzled layout (tile::gather4 moved one 128-byte row in about 19
-// cycles here, which bound the first version of this kernel at 221 TFLOP/s; zero rows for indices
-// outside x come from cp.async's zero fill); one thread of the leader's warp 1 issues the MMAs; warps
-// 2..5 turn each 32 rows of the accumulator around through shared memory and write whole row pieces
-// while the next tile is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
+// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 6..13 copy gathered rows with
+// cp.async and warps 14, 15 hand them over; one thread of the leader's warp 1 issues the MMAs; warps 2..5
+// turn each 32 rows of the accumulator around through shared memory and write whole row pieces while the
+// next tile is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
+//
+// Gathered rows, at 8 experts of 1024 rows, K = 4096, n = 14336 (rows side by side: 1379 TFLOP/s): TMA's
+// tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into registers two stages
+// ahead, 897 (more of them in flight were slower: they need lines of the little L1 that is left);
+// cp.async by four warps, 922, by eight, 1089, by sixteen, 1076; with one k-block a stage, 1040.
+//
+// A stage's barrier lives in the leader, which alone announces the bytes of both CTAs' TMA loads (they are
+// equal): a second announcement from the other CTA cost a fifth of the rate (1058 against 1351 TFLOP/s).
 //
 // A wait that runs out is agreed on by the four epilogue warps before any of them leaves, since they meet
 // at a named barrier.
@@ -30,7 +36,8 @@ constexpr uint32_t HALF = 128 * BK * 2;             // one k-block of one operan
 constexpr uint32_t BOX = 64 * BK * 2;               // 64 columns x 64 k: 8 KiB
 constexpr uint32_t OP_STAGE = KB * HALF;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int THREADS = 320;
+constexpr int LOADERS = 8, RELAYS = 2;              // warps that fetch gathered rows, and that pass them on
+constexpr int THREADS = 192 + 32 * (LOADERS + RELAYS);   // after TMA, MMA and four epilogue warps
 constexpr int STG_LD = 128 + 4;                     // floats between staged rows
 constexpr uint32_t STAGING = 32 * STG_LD * 4;
 constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + STAGING + 256 + (TP_MAX_EXPERTS + 4) * 4;
@@ -38,7 +45,7 @@ constexpr unsigned long long DRAIN = 400000000ull;
 
 struct Pair {
   uint8_t *sW, *sX;
-  uint32_t full0, empty0, accf0, acce0, drain, full0_leader, acce0_leader;
+  uint32_t full0, empty0, rows0, accf0, acce0, drain, full0_leader, acce0_leader;
   volatile uint32_t* abort_flag;
   uint32_t rank;
 };
@@ -49,16 +56,23 @@ __device__ __forceinline__ bool pair_fail(const RaggedParams& p, const Pair& c, 
   return false;
 }
 
-// Bounded wait of a whole warp on a barrier that the other CTA may arrive on; all lanes agree.
+// Bounded waits of one thread, on a barrier that this CTA's threads and copies arrive on, and on one
+// that the other CTA's do too.
+__device__ __forceinline__ bool lane_wait(const RaggedParams& p, const Pair& c, uint32_t bar, uint32_t parity, uint32_t site) {
+  return mbar_wait_bounded(bar, parity, p.budget, c.abort_flag) ? true : pair_fail(p, c, site);
+}
+__device__ __forceinline__ bool lane_wait_cluster(const RaggedParams& p, const Pair& c, uint32_t bar, uint32_t parity,
+                                                  uint32_t site) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!*c.abort_flag && static_cast<unsigned long long>(clock64() - t0) <= p.budget)
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+  return pair_fail(p, c, site);
+}
+// The same of a whole warp: all lanes agree.
 __device__ __forceinline__ bool warp_wait(const RaggedParams& p, const Pair& c, uint32_t bar, uint32_t parity, uint32_t site) {
-  bool got = mbar_try_wait_cluster(bar, parity);
-  if (!__all_sync(0xffffffffu, got)) {
-    const long long t0 = clock64();
-    while (!got && !*c.abort_flag && static_cast<unsigned long long>(clock64() - t0) <= p.budget)
-      got = mbar_try_wait_cluster(bar, parity);
-    got = __all_sync(0xffffffffu, got);
-  }
-  return got ? true : pair_fail(p, c, site);
+  const bool got = mbar_wait_bounded(bar, parity, p.budget, c.abort_flag);
+  return __all_sync(0xffffffffu, got) ? true : pair_fail(p, c, site);
 }
 
 struct Tile {
@@ -115,7 +129,7 @@ __device__ __forceinline__ int next_adapter(const int* off, int L, int i0, int v
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 template <bool SWIGLU, bool LORA>
@@ -132,10 +146,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * OP_STAGE + STAGING);
   c.full0 = smem_u32(bars);
   c.empty0 = c.full0 + 8 * STAGES;
-  c.accf0 = c.empty0 + 8 * STAGES;
+  c.rows0 = c.empty0 + 8 * STAGES;
+  c.accf0 = c.rows0 + 8 * STAGES;
   c.acce0 = c.accf0 + 16;
   c.drain = c.acce0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5);
   c.abort_flag = tmem_slot + 1;
   int* s_off = reinterpret_cast<int*>(bars + 32);
   c.rank = cluster_ctarank();
@@ -144,9 +159,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefetch_tmap(&p.tw);
     if (SWIGLU) prefetch_tmap(&p.tw2);
     if (LORA) prefetch_tmap(&p.tb);
-    if (!gather) prefetch_tmap(&p.tx_box);
+    if (!gather) {
+      prefetch_tmap(&p.tx_box);
+      prefetch_tmap(&p.tx_box32);
+    }
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(c.full0 + 8 * s, gather ? 10 : 2);   // both CTAs' TMA warps, and their four row loaders
+      mbar_init(c.full0 + 8 * s, gather ? 3 : 1);    // the leader's TMA thread, and a relay of each CTA
+      mbar_init(c.rows0 + 8 * s, 32 * LOADERS);
       mbar_init(c.empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -183,22 +202,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!t.live) break;
       const int col = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
       const int nh = t.n_mma / 2, row0 = t.i0 + static_cast<int>(c.rank) * nh;
-      const int boxes = gather ? 0 : (nh + 31) / 32;
+      // rows side by side: one box of 128 rows, or (a low tile) as many of 32 as it takes
+      const uint32_t x_bytes = gather ? 0u : nh > 96 ? HALF : static_cast<uint32_t>((nh + 31) / 32) * 4096u;
       const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
       const int total_kb = p.num_kb + (chunks + 1) / 2;
       int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
-      for (int kb = 0; kb < total_kb; kb += KB) {
-        ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
-        if (!ok) break;
-        if (lane == 0) {
+      if (lane == 0) {
+        for (int kb = 0; kb < total_kb; kb += KB) {
+          ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+          if (!ok) break;
           const uint32_t fb = c.full0_leader + 8 * st;
           uint32_t bytes = 0;
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
-            if (kb + h < p.num_kb) bytes += HALF + boxes * 4096u;
+            if (kb + h < p.num_kb) bytes += HALF + x_bytes;
             else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 4096u;
           }
-          mbar_arrive_expect_tx_cluster(fb, bytes);
+          if (c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, 2 * bytes);   // both CTAs load alike
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
             const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
@@ -210,7 +230,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 tma_load_3d_pair(w, &p.tw, col, k0, t.e, fb);
                 tma_load_3d_pair(w + BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? col : col + 64, k0, t.e, fb);
               }
-              for (int b = 0; b < boxes; ++b) tma_load_2d_pair(x + 4096u * b, &p.tx_box, k0, row0 + 32 * b, fb);
+              if (x_bytes == HALF) tma_load_2d_pair(x, &p.tx_box, k0, row0, fb);
+              else if (!LORA)
+                for (int b = 0; b < static_cast<int>(x_bytes / 4096u); ++b)
+                  tma_load_2d_pair(x + 4096u * b, &p.tx_box32, k0, row0 + 32 * b, fb);
             } else if (LORA && kb + h < total_kb) {
               const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
               for (int ch = 0; ch < nch; ++ch) {
@@ -220,11 +243,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               }
             }
           }
+          ++loaded;
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
-        __syncwarp();
-        ++loaded;
-        if (++st == STAGES) { st = 0; phase ^= 1u; }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (warp == 1) {
     if (c.rank == 0) {
@@ -238,14 +261,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int total_kb = p.num_kb + (chunks + 1) / 2;
         const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !p.w_km, false);
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
-        ok = warp_wait(p, c, c.acce0 + 8 * acc, acc_phase ^ 1u, WAIT_MMA_ACC_EMPTY);
-        if (!ok) break;
-        tc_fence_after();
-        for (int kb = 0; kb < total_kb; kb += KB) {
-          ok = warp_wait(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
-          if (!ok) break;
+        if (lane == 0) {
+          ok = lane_wait_cluster(p, c, c.acce0 + 8 * acc, acc_phase ^ 1u, WAIT_MMA_ACC_EMPTY);
           tc_fence_after();
-          if (lane == 0) {
+          for (int kb = 0; ok && kb < total_kb; kb += KB) {
+            ok = lane_wait_cluster(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int h = 0; h < KB; ++h) {
               const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
@@ -264,13 +286,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
               }
             }
+            mma_issued = true;
             umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
             if (kb + KB >= total_kb) umma_commit_pair_mc(c.accf0 + 8 * acc, 0x3);
+            if (++st == STAGES) { st = 0; phase ^= 1u; }
           }
-          __syncwarp();
-          mma_issued = true;
-          if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
     }
@@ -338,12 +360,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-  } else if (gather) {
-    // Row loaders: eight lanes fetch one row's 128 bytes of a k-block; a stage is handed over when its
-    // copies have landed, one stage after they were issued.
+  } else if (gather && warp < 6 + LOADERS) {
+    // Row loaders: eight lanes copy one row's 128 bytes of a k-block. The copies arrive on this CTA's
+    // barrier when they have landed.
     const int tid = threadIdx.x - 192;
+    constexpr int STEP = LOADERS * 4;                  // rows of one pass
     const int piece = tid & 7, r0 = tid >> 3;
-    int st = 0, pending = -1;
+    int st = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
@@ -351,10 +374,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!t.live) break;
       const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
       const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
-      int idx[8];
+      int idx[128 / STEP];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = r0 + 16 * i;
+      for (int i = 0; i < 128 / STEP; ++i) {
+        const int row = r0 + STEP * i;
         idx[i] = -2;                                   // no row: left as it is (its column is not read)
         if (row < mine) {
           const int r = __ldg(p.row_index + t.i0 + half0 + row);
@@ -372,20 +395,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           uint8_t* x = c.sX + st * OP_STAGE + h * HALF;
           if (kb + h < p.num_kb) {
             const int k = (kb + h) * BK + piece * 8;
-            const bool in_k = k < p.K;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = r0 + 16 * i;
+            for (int i = 0; i < 128 / STEP; ++i) {
+              const int row = r0 + STEP * i;
               if (idx[i] != -2) {
-                const bool fetch = in_k && idx[i] >= 0;
-                const uint16_t* src = fetch ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x;
-                cp_async16(smem_u32(x) + row * 128 + ((piece ^ (row & 7)) << 4), src, fetch ? 16u : 0u);
+                const bool in = k < p.K && idx[i] >= 0;
+                cp_async16(smem_u32(x) + row * 128 + ((piece ^ (row & 7)) << 4),
+                           in ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x, in ? 16u : 0u);
               }
             }
           } else if (LORA && kb + h < total_kb) {
             const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
             for (int ch = 0; ch < nch; ++ch) {
-              for (int it = tid; it < 2 * nh; it += 128) {
+              for (int it = tid; it < 2 * nh; it += 32 * LOADERS) {
                 const int row = it >> 1, sub = it & 1;
                 const int i = t.i0 + half0 + row, k0 = q * 16 + sub * 8;
                 uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
@@ -400,22 +422,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
           }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (pending >= 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(c.full0_leader + 8 * pending);
+        if (LORA && kb + KB > p.num_kb && total_kb > p.num_kb) {   // holds rows of v, written by ordinary stores
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          mbar_arrive(c.rows0 + 8 * st);
+        } else {
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.rows0 + 8 * st) : "memory");
         }
-        pending = st;
         if (++st == STAGES) { st = 0; phase ^= 1u; }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (ok && pending >= 0) {
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(c.full0_leader + 8 * pending);
+  } else if (gather) {
+    // Relays, the stages in turn: what the loaders wrote is ordered before the tensor cores' reads and
+    // passed on to the leader's barrier. (The loaders cannot do it themselves: a release to the other CTA
+    // waits for every copy that its thread has in flight.)
+    const int mine = warp - 6 - LOADERS;
+    int st = 0, turn = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok; u += pairs) {
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      if (!t.live) break;
+      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+      const int total_kb = p.num_kb + (chunks + 1) / 2;
+      if (lane == 0) {
+        for (int kb = 0; kb < total_kb; kb += KB) {
+          if (turn == mine) {
+            ok = lane_wait(p, c, c.rows0 + 8 * st, phase, WAIT_MMA_FULL);
+            if (!ok) break;
+            fence_proxy_async();
+            if (c.rank == 0) mbar_arrive(c.full0 + 8 * st);
+            else mbar_arrive_cluster(c.full0_leader + 8 * st);
+          }
+          if (++turn == RELAYS) turn = 0;
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   }
   // all pair MMAs done, then both CTAs meet before either frees TMEM or exits. After a wait that ran
