@@ -159,32 +159,47 @@ __device__ __forceinline__ float apply_act(float x, int act) {
   return act == TP_ACT_GELU ? gelu_erf(x) : act == TP_ACT_GELU_TANH ? gelu_tanh(x) : x;
 }
 
+// Backward: what the activation was applied to at eight columns of one row (h1: SwiGLU's up half), and the
+// gradient there.
+__device__ __forceinline__ void load_h_pre(const RaggedParams& p, int64_t row, int col, uint4& h0, uint4& h1) {
+  if (p.act == TP_ACT_SWIGLU) {
+    h0 = ld_nc_v4(p.h_pre + row * 2 * p.n + col);
+    h1 = ld_nc_v4(p.h_pre + row * 2 * p.n + p.n + col);
+  } else if (p.act != TP_ACT_NONE) {
+    h0 = ld_nc_v4(p.h_pre + row * p.n + col);
+  }
+}
+__device__ __forceinline__ void store_backward8(const RaggedParams& p, int64_t row, int col, float (&f)[8], uint4 h0, uint4 h1) {
+  uint16_t* y = static_cast<uint16_t*>(p.y);
+  float h[8];
+  unpack_bf8(h0, h);
+  if (p.act == TP_ACT_SWIGLU) {
+    float up[8], dg[8], du[8];
+    unpack_bf8(h1, up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = 1.0f / (1.0f + __expf(-h[i]));
+      dg[i] = f[i] * up[i] * (s * (1.0f + h[i] * (1.0f - s)));
+      du[i] = f[i] * (h[i] * s);
+    }
+    st_v4(y + row * 2 * p.n + col, pack_bf8(dg));
+    st_v4(y + row * 2 * p.n + p.n + col, pack_bf8(du));
+    return;
+  }
+  if (p.act != TP_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= p.act == TP_ACT_GELU ? gelu_grad(h[i]) : gelu_tanh_grad(h[i]);
+  }
+  st_v4(y + row * p.n + col, pack_bf8(f));
+}
+
 // Eight neighbouring columns of one output row: f the products (SwiGLU: the gate's, u the up's), in
 // binary32 until the one rounding at the store.
 __device__ __forceinline__ void store_row8(const RaggedParams& p, int64_t row, int col, float (&f)[8], float (&u)[8]) {
   if (p.backward) {
-    uint16_t* y = static_cast<uint16_t*>(p.y);
-    if (p.act == TP_ACT_SWIGLU) {
-      float g[8], up[8], dg[8], du[8];
-      unpack_bf8(ld_nc_v4(p.h_pre + row * 2 * p.n + col), g);
-      unpack_bf8(ld_nc_v4(p.h_pre + row * 2 * p.n + p.n + col), up);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float s = 1.0f / (1.0f + __expf(-g[i]));
-        dg[i] = f[i] * up[i] * (s * (1.0f + g[i] * (1.0f - s)));
-        du[i] = f[i] * (g[i] * s);
-      }
-      st_v4(y + row * 2 * p.n + col, pack_bf8(dg));
-      st_v4(y + row * 2 * p.n + p.n + col, pack_bf8(du));
-      return;
-    }
-    if (p.act != TP_ACT_NONE) {
-      float h[8];
-      unpack_bf8(ld_nc_v4(p.h_pre + row * p.n + col), h);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= p.act == TP_ACT_GELU ? gelu_grad(h[i]) : gelu_tanh_grad(h[i]);
-    }
-    st_v4(y + row * p.n + col, pack_bf8(f));
+    uint4 h0 = make_uint4(0, 0, 0, 0), h1 = h0;
+    load_h_pre(p, row, col, h0, h1);
+    store_backward8(p, row, col, f, h0, h1);
     return;
   }
   if (p.act == TP_ACT_SWIGLU) {

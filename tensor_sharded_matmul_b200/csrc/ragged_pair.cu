@@ -5,10 +5,10 @@
 // its N, in steps of 32, each CTA holding half of them. A segment of r rows is cut into ceil(r / 256)
 // tiles of nearly equal height, so that its last tile is not a sliver that streams all of W for a few rows.
 //
-// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 6..13 copy gathered rows with
-// cp.async and warps 14, 15 hand them over; one thread of the leader's warp 1 issues the MMAs; warps 2..5
-// turn each 32 rows of the accumulator around through shared memory and write whole row pieces while the
-// next tile is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
+// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 10..17 copy gathered rows with
+// cp.async and warps 18, 19 hand them over; one thread of the leader's warp 1 issues the MMAs; warps 2..9
+// turn the accumulator's rows around through shared memory and write whole row pieces while the next tile
+// is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
 //
 // Gathered rows, at 8 experts of 1024 rows, K = 4096, n = 14336 (rows side by side: 1379 TFLOP/s): TMA's
 // tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into registers two stages
@@ -37,9 +37,12 @@ constexpr uint32_t BOX = 64 * BK * 2;               // 64 columns x 64 k: 8 KiB
 constexpr uint32_t OP_STAGE = KB * HALF;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int LOADERS = 8, RELAYS = 2;              // warps that fetch gathered rows, and that pass them on
-constexpr int THREADS = 192 + 32 * (LOADERS + RELAYS);   // after TMA, MMA and four epilogue warps
+constexpr int EPI = 8;                              // epilogue warps: two groups of four
+constexpr int LOAD0 = 2 + EPI, RELAY0 = LOAD0 + LOADERS;   // first warps; before them TMA, MMA, epilogue
+constexpr int THREADS = 32 * (RELAY0 + RELAYS);
 constexpr int STG_LD = 128 + 4;                     // floats between staged rows
-constexpr uint32_t STAGING = 32 * STG_LD * 4;
+constexpr int CHUNK = 16;                           // rows that a group turns around at a time
+constexpr uint32_t STAGING = 2 * CHUNK * STG_LD * 4;
 constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + STAGING + 256 + (TP_MAX_EXPERTS + 4) * 4;
 constexpr unsigned long long DRAIN = 400000000ull;
 
@@ -170,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(c.accf0 + 8 * a, 1);
-      mbar_init(c.acce0 + 8 * a, 8);                 // epilogue warps of both CTAs
+      mbar_init(c.acce0 + 8 * a, 2 * EPI);           // epilogue warps of both CTAs
     }
     mbar_init(c.drain, 1);
     *c.abort_flag = 0u;
@@ -296,55 +299,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
     }
-  } else if (warp < 6) {
-    const int quad = warp & 3;
-    const int tid = threadIdx.x - 64;
-    constexpr int GROUPS = SWIGLU ? 8 : 16;
+  } else if (warp < LOAD0) {
+    // Two groups of four warps, one TMEM lane quadrant each, take the tile's rows 16 at a time in turn.
+    const int quad = warp & 3, group = (warp - 2) >> 2;
+    const int tid = (threadIdx.x - 64) & 127;
+    float* stg = staging + group * CHUNK * STG_LD;
+    constexpr int GROUPS = SWIGLU ? 8 : 16;           // eight columns each
+    constexpr int ITEMS = CHUNK * GROUPS / 128;       // of a chunk, for each thread
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int u = pair;; u += pairs) {
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
       if (!t.live) break;
       const int col0 = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
+      // h_pre of the group's next chunk is on its way while this one is finished (it comes from DRAM)
+      uint4 h0[ITEMS], h1[ITEMS];
+      auto fetch_h = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+          const int it = tid + 128 * k, j = j0 + it / GROUPS, col = col0 + (it % GROUPS) * 8;
+          if (j < t.valid && col < p.n) load_h_pre(p, t.i0 + j, col, h0[k], h1[k]);
+        }
+      };
+      if (!SWIGLU && !LORA && p.backward) fetch_h(group * CHUNK);
       int got = warp_wait(p, c, c.accf0 + 8 * acc, acc_phase, WAIT_EPI_ACC_FULL) ? 1 : 0;
-      // all four warps go on, or none
+      // all warps go on, or none
       asm volatile(
           "{\n\t.reg .pred p, q;\n\t"
           "setp.ne.s32 p, %0, 0;\n\t"
-          "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+          "barrier.cta.red.and.pred q, 3, 256, p;\n\t"
           "selp.s32 %0, 1, 0, q;\n\t}\n"
           : "+r"(got)::"memory");
       if (!got) break;
       tc_fence_after();
       const uint32_t tm = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256);
-      for (int j0 = 0; j0 < t.valid; j0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(tm + j0, v);
+      bool held = true;
+      for (int j0 = group * CHUNK; j0 < t.valid; j0 += 2 * CHUNK) {
+        uint32_t v[CHUNK];
+        tmem_ld16(tm + j0, v);
         tmem_ld_wait();
-        if (j0 + 32 >= t.valid) {                     // the accumulator is read: the next tile may have it
+        if (j0 + 2 * CHUNK >= t.valid) {              // this warp's part is read: the next tile may have it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(c.acce0_leader + 8 * acc);
+          held = false;
         }
-        float* s = staging + quad * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[j * STG_LD] = __uint_as_float(v[j]);
-        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-        const int items = min(32, t.valid - j0) * GROUPS;
-        for (int it = tid; it < items; it += 128) {
-          const int j = it / GROUPS, c8 = (it % GROUPS) * 8;
-          const int col = col0 + c8;
-          if (col >= p.n) continue;
-          float f[8], up[8];
-          const float4* src = reinterpret_cast<const float4*>(staging + j * STG_LD + c8);
-          *reinterpret_cast<float4*>(f) = src[0];
-          *reinterpret_cast<float4*>(f + 4) = src[1];
-          if constexpr (SWIGLU) {
-            *reinterpret_cast<float4*>(up) = src[16];
-            *reinterpret_cast<float4*>(up + 4) = src[17];
+        for (int j = 0; j < CHUNK; ++j) stg[j * STG_LD + quad * 32 + lane] = __uint_as_float(v[j]);
+        asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+        float4 f4[ITEMS][2], u4[ITEMS][2];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+          const int it = tid + 128 * k;
+          const float4* src = reinterpret_cast<const float4*>(stg + (it / GROUPS) * STG_LD + (it % GROUPS) * 8);
+          f4[k][0] = src[0];
+          f4[k][1] = src[1];
+          u4[k][0] = SWIGLU ? src[16] : src[0];
+          u4[k][1] = SWIGLU ? src[17] : src[1];
+        }
+        asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory");
+        uint4 g0[ITEMS], g1[ITEMS];
+        if (!SWIGLU && !LORA && p.backward) {
+#pragma unroll
+          for (int k = 0; k < ITEMS; ++k) {
+            g0[k] = h0[k];
+            g1[k] = h1[k];
           }
-          const int i = t.i0 + j0 + j;
-          if (p.seg_scale != nullptr) {
+          fetch_h(j0 + 2 * CHUNK);
+        }
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+          const int it = tid + 128 * k;
+          const int j = j0 + it / GROUPS, col = col0 + (it % GROUPS) * 8;
+          if (j >= t.valid || col >= p.n) continue;
+          float f[8] = {f4[k][0].x, f4[k][0].y, f4[k][0].z, f4[k][0].w, f4[k][1].x, f4[k][1].y, f4[k][1].z, f4[k][1].w};
+          float up[8] = {u4[k][0].x, u4[k][0].y, u4[k][0].z, u4[k][0].w, u4[k][1].x, u4[k][1].y, u4[k][1].z, u4[k][1].w};
+          const int i = t.i0 + j;
+          if (!SWIGLU && !LORA && p.backward) {
+            store_backward8(p, i, col, f, g0[k], g1[k]);
+            continue;
+          }
+          if (!LORA && p.seg_scale != nullptr) {
             const float sc = __ldg(p.seg_scale + t.e);
 #pragma unroll
             for (int q = 0; q < 8; ++q) f[q] *= sc;
@@ -356,14 +391,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             store_row8(p, i, col, f, up);
           }
         }
-        asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+      }
+      if (held) {                                     // a low tile: the other group had all of it
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(c.acce0_leader + 8 * acc);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-  } else if (gather && warp < 6 + LOADERS) {
+  } else if (gather && warp < RELAY0) {
     // Row loaders: eight lanes copy one row's 128 bytes of a k-block. The copies arrive on this CTA's
     // barrier when they have landed.
-    const int tid = threadIdx.x - 192;
+    const int tid = threadIdx.x - 32 * LOAD0;
     constexpr int STEP = LOADERS * 4;                  // rows of one pass
     const int piece = tid & 7, r0 = tid >> 3;
     int st = 0;
@@ -436,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // Relays, the stages in turn: what the loaders wrote is ordered before the tensor cores' reads and
     // passed on to the leader's barrier. (The loaders cannot do it themselves: a release to the other CTA
     // waits for every copy that its thread has in flight.)
-    const int mine = warp - 6 - LOADERS;
+    const int mine = warp - RELAY0;
     int st = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
