@@ -1255,6 +1255,19 @@ bool encode_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_out_3d(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t count) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[3] = {cols, rows, count};
+  cuuint64_t strides[2] = {cols * size, cols * rows * size};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // Reserve the dynamic shared memory of a kernel once per device.

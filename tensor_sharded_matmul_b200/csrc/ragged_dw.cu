@@ -35,9 +35,9 @@ constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + 8 * STG_WARP + 256;
 struct DwParams {
   CUtensorMap tx, tx_row;      // x [x_rows][k]: 64 x 64 boxes, and boxes one row high
   CUtensorMap td, td_row;      // dy [R][n]
+  CUtensorMap tdw;             // dw [E][k][n], 32 x 32 boxes
   const int32_t* offsets;
   const int32_t* row_index;
-  void* dw;
   int R, x_rows, E, k, n, tiles_k, tiles_n, units;
   bool out_f32;
   uint32_t* status;
@@ -116,6 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefetch_tmap(&p.tx_row);
     prefetch_tmap(&p.td);
     prefetch_tmap(&p.td_row);
+    prefetch_tmap(&p.tdw);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(c.full0 + 8 * s, 1);
       mbar_init(c.empty0 + 8 * s, 1);
@@ -264,37 +265,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) break;
-      // one row a lane -> whole 128-byte row pieces, through this warp's staging buffer
-      const int sub = lane & 7;
+      // 32 x 32 blocks, one row a lane, swizzled into this warp's staging buffer and stored by TMA, which
+      // leaves out what lies outside dW_e. (16-byte stores from the threads held the kernel at 446
+      // TFLOP/s where it runs at 1032 without any, at 64 experts of 384 rows, 1024 x 2048.)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                       "f"(sum[q][4 * j]), "f"(sum[q][4 * j + 1]), "f"(sum[q][4 * j + 2]), "f"(sum[q][4 * j + 3])
-                       : "memory");
+        bulk_wait_read();                          // lane 0: the last block has left the buffer
         __syncwarp();
+        if (p.out_f32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 4 * j + (lane >> 3);
-          float4 x;
-          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                       : "r"(stg + r * 128 + ((sub ^ (r & 7)) << 4))
-                       : "memory");
-          const int row = row0 + r, col = col0 + q * 32 + 4 * sub;
-          if (row < p.k && col < p.n) {
-            const int64_t at = (static_cast<int64_t>(e) * p.k + row) * p.n + col;
-            if (p.out_f32)
-              st_v4(static_cast<float*>(p.dw) + at,
-                    make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)));
-            else
-              st_v2(static_cast<uint16_t*>(p.dw) + at, make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w)));
-          }
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                         "f"(sum[q][4 * j]), "f"(sum[q][4 * j + 1]), "f"(sum[q][4 * j + 2]), "f"(sum[q][4 * j + 3])
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(pack_bf2(sum[q][8 * j], sum[q][8 * j + 1])), "r"(pack_bf2(sum[q][8 * j + 2], sum[q][8 * j + 3])),
+                         "r"(pack_bf2(sum[q][8 * j + 4], sum[q][8 * j + 5])), "r"(pack_bf2(sum[q][8 * j + 6], sum[q][8 * j + 7]))
+                         : "memory");
         }
+        fence_proxy_async();
         __syncwarp();
+        if (lane == 0 && row0 < p.k && col0 + q * 32 < p.n) {
+          tma_store_3d(&p.tdw, stg, col0 + q * 32, row0, e);
+          bulk_commit();
+        }
       }
     }
+    bulk_wait();
   }
   // all pair MMAs done, then both CTAs meet before either frees TMEM or exits. After a wait that ran
   // out, the copies still in flight land first (they count on the leader's barriers).
@@ -323,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
   DwParams p;
   std::memset(&p, 0, sizeof(p));
-  p.offsets = g.offsets; p.row_index = g.row_index; p.dw = g.dw;
+  p.offsets = g.offsets; p.row_index = g.row_index;
   p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
   p.E = g.E; p.k = static_cast<int>(g.k); p.n = static_cast<int>(g.n);
   p.tiles_k = (p.k + 255) / 256;
@@ -335,6 +335,7 @@ tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
   if (!encode_bf16_2d(&p.tx, g.x, g.k, g.x_rows, g.k, 64, 64) || !encode_bf16_2d(&p.tx_row, g.x, g.k, g.x_rows, g.k, 64, 1) ||
       !encode_bf16_2d(&p.td, g.dy, g.n, g.R, g.n, 64, 64) || !encode_bf16_2d(&p.td_row, g.dy, g.n, g.R, g.n, 64, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptors");
+  if (!encode_out_3d(&p.tdw, g.dw, g.out_f32, g.n, g.k, g.E)) return fail(TP_ECUDA, "cannot encode the TMA descriptor of dW");
   p.status = status_word();
   p.budget = wait_budget();
   if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");

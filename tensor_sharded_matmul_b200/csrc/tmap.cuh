@@ -18,4 +18,8 @@ bool encode_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t o
 bool encode_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t count, uint64_t ld,
                     uint32_t box_inner, uint32_t box_rows);
 
+// 3-D view [count, rows, cols] of a contiguous fp32 or bf16 output for stores of 32 x 32 boxes, whose rows of 128 (64)
+// bytes lie swizzled in shared memory with the pattern of that width.
+bool encode_out_3d(CUtensorMap* m, void* base, bool f32, uint64_t cols, uint64_t rows, uint64_t count);
+
 }  // namespace tpx
