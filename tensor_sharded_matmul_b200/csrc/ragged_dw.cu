@@ -2,10 +2,10 @@
 //
 // Here the ragged dimension is the contraction. CTA pairs (tcgen05 cta_group::2) compute 256 x 256 tiles
 // of dW_e, each CTA holding 128 of x's columns and 128 of dy's per 64-row k-block; both operands are
-// M-major as they lie in memory. Whole k-blocks come by TMA (x's rows four at a time by index when
-// they are gathered). A segment's last, partial k-block is loaded row by row, and the rest of the tile from
-// rows past the end of the matrix, which TMA reads as zeros: in both operands, so that a
-// neighbour's rows (whatever they hold) never enter.
+// M-major as they lie in memory. Whole k-blocks come by TMA; gathered rows of x by cp.async (see
+// ragged_pair.cu). A segment's last, partial k-block is loaded row by row, and the rest of the tile from
+// rows past the end of the matrix, which TMA reads as zeros (cp.async: its zero fill): in both operands, so
+// that a neighbour's rows (whatever they hold) never enter.
 //
 // Tensor cores add each K=16 step to the accumulator with truncation: over a long contraction the
 // sum is short by about K / 32 times 2^-24 of itself (measured 4.4e-6 at K = 4096, 1.9e-5 at 16384).
@@ -28,7 +28,12 @@ constexpr uint32_t BOX = 64 * BK * 2;                // 64 columns x 64 rows: 8 
 constexpr uint32_t OP_STAGE = KB * HALF;             // 32 KiB
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int SPAN_KB = 8;                           // k-blocks per accumulator span (512 rows)
-constexpr int THREADS = 320;                         // loads, MMA, 8 epilogue warps
+constexpr int LOADERS = 4;                           // warps that copy gathered rows
+// TMA and MMA warps, two relays (gathered rows), eight epilogue warps, the loaders.
+template <bool GATHER>
+constexpr int EPI0 = GATHER ? 4 : 2;
+template <bool GATHER>
+constexpr int THREADS = 32 * (EPI0<GATHER> + 8 + (GATHER ? LOADERS : 0));
 constexpr uint32_t STG_WARP = 32 * 128;
 constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + 8 * STG_WARP + 256;
 
@@ -38,6 +43,7 @@ struct DwParams {
   CUtensorMap tdw;             // dw [E][k][n], 32 x 32 boxes
   const int32_t* offsets;
   const int32_t* row_index;
+  const uint16_t* x;
   int R, x_rows, E, k, n, tiles_k, tiles_n, units;
   bool out_f32;
   uint32_t* status;
@@ -46,7 +52,7 @@ struct DwParams {
 
 struct Dw {
   uint8_t *sA, *sB;
-  uint32_t full0, empty0, accf0, acce0, drain, full0_leader, acce0_leader;
+  uint32_t full0, empty0, rows0, accf0, acce0, drain, full0_leader, acce0_leader;
   volatile uint32_t* abort_flag;
   uint32_t rank;
 };
@@ -57,42 +63,26 @@ __device__ __forceinline__ bool dw_fail(const DwParams& p, const Dw& c, uint32_t
   return false;
 }
 
-// One 64-row k-block of one operand (this CTA's 128 columns from x0): rows r0 .. r0 + v - 1 of the
-// sorted order, and zeros for the other rows of the tile and for indices outside 0 .. limit - 1 (a row past
-// the matrix reads as zeros). Whole warp; always counts 16 KiB.
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row,
-                                             const int32_t* index, int limit, int x0, int r0, int v, uint32_t fb, int lane) {
-  const int half = lane >> 4, grp = lane & 15;
-  if (v == BK && index == nullptr) {
+// One 64-row k-block of one operand by TMA (this CTA's 128 columns from x0): rows r0 .. r0 + v - 1, and
+// zeros for the other rows of the tile (a row past the matrix, `limit`, reads as zeros). Whole warp;
+// always counts 16 KiB.
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row, int limit, int x0,
+                                             int r0, int v, uint32_t fb, int lane) {
+  if (v == BK) {
     if (lane < 2) tma_load_2d_pair(dst + lane * BOX, box, x0 + 64 * lane, r0, fb);
-    return;
-  }
-  bool all_in = true;
-  int4 r = make_int4(0, 0, 0, 0);
-  if (index != nullptr && v == BK) {
-    const int i = r0 + 4 * grp;
-    r = make_int4(__ldg(index + i), __ldg(index + i + 1), __ldg(index + i + 2), __ldg(index + i + 3));
-    all_in = r.x >= 0 && r.x < limit && r.y >= 0 && r.y < limit && r.z >= 0 && r.z < limit && r.w >= 0 && r.w < limit;
-  }
-  all_in = __all_sync(0xffffffffu, all_in);
-  if (v == BK && all_in) {
-    tma_gather4_pair(dst + half * BOX + grp * 512u, row, x0 + 64 * half, r.x, r.y, r.z, r.w, fb);
     return;
   }
 #pragma unroll
   for (int j0 = 0; j0 < BK; j0 += 32) {
     const int j = j0 + lane;
-    int at = limit;
-    if (j < v) {
-      at = index != nullptr ? __ldg(index + r0 + j) : r0 + j;
-      if (at < 0 || at > limit) at = limit;
-    }
+    const int at = j < v ? r0 + j : limit;
     tma_load_2d_pair(dst + j * 128u, row, x0, at, fb);
     tma_load_2d_pair(dst + BOX + j * 128u, row, x0 + 64, at, fb);
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+template <bool GATHER>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
     ragged_dw_kernel(const __grid_constant__ DwParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -105,10 +95,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * 2 * OP_STAGE + 8 * STG_WARP);
   c.full0 = smem_u32(bars);
   c.empty0 = c.full0 + 8 * STAGES;
-  c.accf0 = c.empty0 + 8 * STAGES;
+  c.rows0 = c.empty0 + 8 * STAGES;
+  c.accf0 = c.rows0 + 8 * STAGES;
   c.acce0 = c.accf0 + 16;
   c.drain = c.acce0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5);
   c.abort_flag = tmem_slot + 1;
   c.rank = cluster_ctarank();
   if (threadIdx.x == 0) {
@@ -118,7 +109,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefetch_tmap(&p.td_row);
     prefetch_tmap(&p.tdw);
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(c.full0 + 8 * s, 1);
+      mbar_init(c.full0 + 8 * s, GATHER ? 3 : 1);   // the leader's TMA warp, and a relay of each CTA
+      mbar_init(c.rows0 + 8 * s, 32 * LOADERS);
       mbar_init(c.empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -144,7 +136,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   bool mma_issued = false;
   int loaded = 0;                               // warp 0: stages filled
 
-  if (warp == 0) {
+  auto produce = [&]() {
     int st = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -161,21 +153,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           break;
         }
         const uint32_t fb = c.full0_leader + 8 * st;
-        if (lane == 0 && c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, end - r > BK ? 8 * HALF : 4 * HALF);   // of both CTAs
+        if (lane == 0 && c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, (end - r > BK ? 4 : 2) * (GATHER ? 1 : 2) * HALF);   // of both CTAs
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < KB; ++h) {
           const int r0 = r + h * BK, v = min(BK, end - r0);
           if (v <= 0) break;                    // not multiplied either
           const uint32_t off = st * OP_STAGE + h * HALF;
-          load_operand(smem_u32(c.sA + off), &p.tx, &p.tx_row, p.row_index, p.x_rows, a0, r0, v, fb, lane);
-          load_operand(smem_u32(c.sB + off), &p.td, &p.td_row, nullptr, p.R, b0, r0, v, fb, lane);
+          if (!GATHER) load_operand(smem_u32(c.sA + off), &p.tx, &p.tx_row, p.x_rows, a0, r0, v, fb, lane);
+          load_operand(smem_u32(c.sB + off), &p.td, &p.td_row, p.R, b0, r0, v, fb, lane);
         }
         ++loaded;
         if (++st == STAGES) { st = 0; phase ^= 1u; }
       }
     }
-  } else if (warp == 1) {
+  };
+  auto multiply = [&]() {
     if (lane == 0 && c.rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(256, 256, true, true);
       int st = 0, acc = 0;
@@ -225,11 +218,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else {
-    // warps 2..9: TMEM lane quadrant = warp % 4 (rows of dW); warps 2..5 the left 128 columns, 6..9
-    // the right. Each thread holds the running sums of one row's 128 columns.
-    const int quad = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t stg = staging0 + static_cast<uint32_t>(warp - 2) * STG_WARP;
+  };
+  auto relay = [&]() {
+    // Relays, the stages in turn: the loaders' copies are ordered before the tensor cores' reads and passed
+    // on to the leader's barrier.
+    if (lane == 0) {
+      int st = 0, turn = 2;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.units; u += pairs) {
+        const int e = u / per_seg;
+        const int begin = seg_bound(p.offsets, e, p.R), end = seg_bound(p.offsets, e + 1, p.R);
+        for (int r = begin; r < end; r += KB * BK) {
+          if (turn == warp) {
+            if (!mbar_wait_bounded(c.rows0 + 8 * st, phase, p.budget, c.abort_flag)) {
+              ok = dw_fail(p, c, WAIT_MMA_FULL);
+              break;
+            }
+            fence_proxy_async();
+            if (c.rank == 0) mbar_arrive(c.full0 + 8 * st);
+            else mbar_arrive_cluster(c.full0_leader + 8 * st);
+          }
+          turn ^= 1;
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
+        }
+      }
+    }
+  };
+  auto load_rows = [&]() {
+    // Row loaders: sixteen lanes copy one row's 256 bytes of this CTA's columns, zeros for rows past the
+    // segment and for indices outside x. The copies arrive on this CTA's barrier when they have landed.
+    const int tid = threadIdx.x - 32 * (EPI0<GATHER> + 8);
+    constexpr int STEP = 2 * LOADERS;                 // rows of one pass
+    const int piece = tid & 15, row0 = tid >> 4;
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < p.units; u += pairs) {
+      const int e = u / per_seg, local = u - e * per_seg;
+      const int col = (local % p.tiles_k) * 256 + static_cast<int>(c.rank) * 128 + piece * 8;
+      const int begin = seg_bound(p.offsets, e, p.R), end = seg_bound(p.offsets, e + 1, p.R);
+      for (int r = begin; r < end; r += KB * BK) {
+        int idx[KB][BK / STEP];
+#pragma unroll
+        for (int h = 0; h < KB; ++h)
+#pragma unroll
+          for (int i = 0; i < BK / STEP; ++i) {
+            const int at = r + h * BK + row0 + STEP * i;
+            idx[h][i] = at < end ? __ldg(p.row_index + at) : -1;
+          }
+        ok = mbar_wait_bounded(c.empty0 + 8 * st, phase ^ 1u, p.budget, c.abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          dw_fail(p, c, WAIT_PRODUCER_EMPTY);
+          break;
+        }
+        const uint32_t dst = smem_u32(c.sA + st * OP_STAGE) + (piece >> 3) * BOX;
+#pragma unroll
+        for (int h = 0; h < KB; ++h) {
+          if (r + h * BK >= end) break;               // not multiplied either
+#pragma unroll
+          for (int i = 0; i < BK / STEP; ++i) {
+            const int row = row0 + STEP * i;
+            const bool in = idx[h][i] >= 0 && idx[h][i] < p.x_rows && col < p.k;
+            const uint16_t* src = in ? p.x + static_cast<int64_t>(idx[h][i]) * p.k + col : p.x;
+            cp_async16(dst + h * HALF + row * 128 + (((piece & 7) ^ (row & 7)) << 4), src, in ? 16u : 0u);
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.rows0 + 8 * st) : "memory");
+        if (++st == STAGES) { st = 0; phase ^= 1u; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  };
+  auto epilogue = [&]() {
+    // Epilogue: TMEM lane quadrant = warp % 4 (rows of dW); the first four warps the left 128 columns, the
+    // others the right. Each thread holds the running sums of one row's 128 columns.
+    const int quad = warp & 3, half = (warp - EPI0<GATHER>) >> 2;
+    const uint32_t stg = staging0 + static_cast<uint32_t>(warp - EPI0<GATHER>) * STG_WARP;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -252,12 +318,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t t = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_ld32(t + q * 32, v);
+        for (int q = 0; q < 8; ++q) {
+          uint32_t v[16];
+          tmem_ld16(t + q * 16, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[q][i] = __fadd_rn(sum[q][i], __uint_as_float(v[i]));
+          for (int i = 0; i < 16; ++i)
+            sum[q / 2][(q % 2) * 16 + i] = __fadd_rn(sum[q / 2][(q % 2) * 16 + i], __uint_as_float(v[i]));
         }
         tc_fence_before();
         __syncwarp();
@@ -295,6 +362,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     bulk_wait();
+  };
+  if constexpr (GATHER) {
+    // The running sums take 128 registers a thread; these 512 threads start at 128 each, and
+    // 256 * 168 + 256 * 56 = 57344 of the 65536 are asked for.
+    if (warp >= 4 && warp < 12) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+      epilogue();
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 0) produce();
+      else if (warp == 1) multiply();
+      else if (warp < 4) relay();
+      else load_rows();
+    }
+  } else {
+    if (warp == 0) produce();
+    else if (warp == 1) multiply();
+    else epilogue();
   }
   // all pair MMAs done, then both CTAs meet before either frees TMEM or exits. After a wait that ran
   // out, the copies still in flight land first (they count on the leader's barriers).
@@ -318,12 +403,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
+template <bool GATHER>
+tp_status launch_dw(const DwParams& p, cudaStream_t s) {
+  static int configured_for[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
+  if (dev < 0 || dev >= 64 || !configured_for[dev]) {
+    if (cudaFuncSetAttribute(ragged_dw_kernel<GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM)) !=
+        cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
+    if (dev >= 0 && dev < 64) configured_for[dev] = 1;
+  }
+  const int sms = sm_count();
+  int grid = 2 * static_cast<int64_t>(p.units) < sms ? 2 * p.units : (sms & ~1);
+  if (grid < 2) grid = 2;
+  ragged_dw_kernel<GATHER><<<grid, THREADS<GATHER>, SMEM, s>>>(p);
+  return check_launch("ragged_dw_kernel");
+}
+
 }  // namespace
 
 tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
   DwParams p;
   std::memset(&p, 0, sizeof(p));
-  p.offsets = g.offsets; p.row_index = g.row_index;
+  p.offsets = g.offsets; p.row_index = g.row_index; p.x = g.x;
   p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
   p.E = g.E; p.k = static_cast<int>(g.k); p.n = static_cast<int>(g.n);
   p.tiles_k = (p.k + 255) / 256;
@@ -339,19 +442,7 @@ tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
   p.status = status_word();
   p.budget = wait_budget();
   if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");
-  static int configured_for[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
-  if (dev < 0 || dev >= 64 || !configured_for[dev]) {
-    if (cudaFuncSetAttribute(ragged_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM)) != cudaSuccess)
-      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
-    if (dev >= 0 && dev < 64) configured_for[dev] = 1;
-  }
-  const int sms = sm_count();
-  int grid = 2 * units < sms ? static_cast<int>(2 * units) : (sms & ~1);
-  if (grid < 2) grid = 2;
-  ragged_dw_kernel<<<grid, THREADS, SMEM, s>>>(p);
-  return check_launch("ragged_dw_kernel");
+  return g.row_index != nullptr ? launch_dw<true>(p, s) : launch_dw<false>(p, s);
 }
 
 }  // namespace tpx

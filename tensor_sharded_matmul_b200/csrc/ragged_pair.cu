@@ -131,10 +131,6 @@ __device__ __forceinline__ int next_adapter(const int* off, int L, int i0, int v
   return a;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 template <bool SWIGLU, bool LORA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ragged_pair_kernel(const __grid_constant__ RaggedParams p) {
