@@ -122,10 +122,30 @@ def _ptrs(xs):
     return C.cast(arr, _pp)
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream of the current device as an address (None without a GPU). torch's raw getter spares
+    the stream object that current_stream() builds: 0.4 against 3.9 us a call."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None:
+            _raw_stream = lambda: raw(device())                            # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -317,17 +317,28 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const void* __restrict__
 }
 
 // ------------------------------------------------------------------ combine
+// Eight values as loaded, converted when they are used.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* base, int64_t at, float (&f)[8]) {
-  if constexpr (BF16) {
-    unpack_bf8(ld_nc_v4(static_cast<const uint16_t*>(base) + at), f);
-  } else {
-    const uint4 a = ld_nc_v4(static_cast<const float*>(base) + at);
-    const uint4 b = ld_nc_v4(static_cast<const float*>(base) + at + 4);
-    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+struct Raw8 {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t at) {
+    if constexpr (BF16) {
+      a = ld_nc_v4(static_cast<const uint16_t*>(base) + at);
+    } else {
+      a = ld_nc_v4(static_cast<const float*>(base) + at);
+      b = ld_nc_v4(static_cast<const float*>(base) + at + 4);
+    }
   }
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (BF16) {
+      unpack_bf8(a, f);
+    } else {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 
 template <int KMAX, bool U_BF16, bool Y_BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u, int64_t R, const float* __restrict__ weight,
@@ -343,21 +354,23 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += KMAX) {
-      float f[KMAX][8];
+      Raw8<U_BF16> raw[KMAX];
       float w[KMAX];
 #pragma unroll
       for (int j = 0; j < KMAX; ++j) {
         const int s = j0 + j < k ? __ldg(slot + n * k + j0 + j) : -1;
         const bool in = s >= 0 && s < R;
         w[j] = !in ? 0.0f : weight != nullptr ? __ldg(weight + n * k + j0 + j) : 1.0f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[j][q] = 0.0f;
-        if (in) load8<U_BF16>(u, static_cast<int64_t>(s) * h + col, f[j]);
+        raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
+        if (in) raw[j].load(u, static_cast<int64_t>(s) * h + col);
       }
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j)
+      for (int j = 0; j < KMAX; ++j) {
+        float f[8];
+        raw[j].get(f);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], f[j][q], acc[q]);
+        for (int q = 0; q < 8; ++q) acc[q] = fmaf(w[j], f[q], acc[q]);
+      }
     }
     if constexpr (Y_BF16) {
       st_v4(static_cast<uint16_t*>(y) + n * h + col, pack_bf8(acc));
@@ -388,19 +401,24 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
   }
   for (int col = lane * 8; col < h; col += 256) {
     float g[8];
-    load8<DY_BF16>(dy, n * h + col, g);
+    Raw8<DY_BF16> dyv;
+    dyv.load(dy, n * h + col);
+    dyv.get(g);
+    Raw8<U_BF16> raw[KMAX];                    // all rows' loads in flight before the first is used
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (s[j] >= 0) raw[j].load(u, static_cast<int64_t>(s[j]) * h + col);
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
       if (s[j] < 0) continue;
-      const int64_t at = static_cast<int64_t>(s[j]) * h + col;
       float f[8], o[8];
-      load8<U_BF16>(u, at, f);
+      raw[j].get(f);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         dot[j] = fmaf(g[q], f[q], dot[j]);
         o[q] = w[j] * g[q];
       }
-      st_v4(du + at, pack_bf8(o));
+      st_v4(du + static_cast<int64_t>(s[j]) * h + col, pack_bf8(o));
     }
   }
 #pragma unroll

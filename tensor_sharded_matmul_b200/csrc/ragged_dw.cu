@@ -3,9 +3,10 @@
 // Here the ragged dimension is the contraction. CTA pairs (tcgen05 cta_group::2) compute 256 x 256 tiles
 // of dW_e, each CTA holding 128 of x's columns and 128 of dy's per 64-row k-block; both operands are
 // M-major as they lie in memory. Whole k-blocks come by TMA; gathered rows of x by cp.async (see
-// ragged_pair.cu). A segment's last, partial k-block is loaded row by row, and the rest of the tile from
-// rows past the end of the matrix, which TMA reads as zeros (cp.async: its zero fill): in both operands, so
-// that a neighbour's rows (whatever they hold) never enter.
+// ragged_pair.cu). A segment's last, partial k-block is put together from boxes of 32, 16, .. 1 rows, and the
+// rest of the tile from boxes past the end of the matrix, which TMA reads as zeros (cp.async: its zero
+// fill): in both operands, so that a neighbour's rows (whatever they hold) never enter. (Single rows
+// alone, 256 loads of about 75 cycles, cost more than the product of a small segment.)
 //
 // Tensor cores add each K=16 step to the accumulator with truncation: over a long contraction the
 // sum is short by about K / 32 times 2^-24 of itself (measured 4.4e-6 at K = 4096, 1.9e-5 at 16384).
@@ -38,8 +39,8 @@ constexpr uint32_t STG_WARP = 32 * 128;
 constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + 8 * STG_WARP + 256;
 
 struct DwParams {
-  CUtensorMap tx, tx_row;      // x [x_rows][k]: 64 x 64 boxes, and boxes one row high
-  CUtensorMap td, td_row;      // dy [R][n]
+  CUtensorMap tx[7];           // x [x_rows][k]: boxes of 64 columns, 64 >> i rows high
+  CUtensorMap td[7];           // dy [R][n]
   CUtensorMap tdw;             // dw [E][k][n], 32 x 32 boxes
   const int32_t* offsets;
   const int32_t* row_index;
@@ -64,20 +65,27 @@ __device__ __forceinline__ bool dw_fail(const DwParams& p, const Dw& c, uint32_t
 }
 
 // One 64-row k-block of one operand by TMA (this CTA's 128 columns from x0): rows r0 .. r0 + v - 1, and
-// zeros for the other rows of the tile (a row past the matrix, `limit`, reads as zeros). Whole warp;
-// always counts 16 KiB.
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* box, const CUtensorMap* row, int limit, int x0,
-                                             int r0, int v, uint32_t fb, int lane) {
+// zeros for the other rows of the tile (a box past the matrix, from row `limit` on, reads as zeros). Two
+// lanes, 64 columns each; always counts 16 KiB. A partial block is put together from boxes of falling
+// height, at most seven a lane.
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* maps, int limit, int x0, int r0, int v,
+                                             uint32_t fb, int lane) {
+  if (lane >= 2) return;
+  const int x = x0 + 64 * lane;
+  dst += lane * BOX;
   if (v == BK) {
-    if (lane < 2) tma_load_2d_pair(dst + lane * BOX, box, x0 + 64 * lane, r0, fb);
+    tma_load_2d_pair(dst, maps, x, r0, fb);
     return;
   }
-#pragma unroll
-  for (int j0 = 0; j0 < BK; j0 += 32) {
-    const int j = j0 + lane;
-    const int at = j < v ? r0 + j : limit;
-    tma_load_2d_pair(dst + j * 128u, row, x0, at, fb);
-    tma_load_2d_pair(dst + BOX + j * 128u, row, x0 + 64, at, fb);
+  for (int part = 0, at = 0; part < 2; ++part) {
+    const int rows = part == 0 ? v : BK - v;
+    for (int i = 1; i < 7; ++i) {
+      const int high = BK >> i;
+      if (rows & high) {
+        tma_load_2d_pair(dst + at * 128u, maps + i, x, part == 0 ? r0 + at : limit, fb);
+        at += high;
+      }
+    }
   }
 }
 
@@ -103,10 +111,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
   c.abort_flag = tmem_slot + 1;
   c.rank = cluster_ctarank();
   if (threadIdx.x == 0) {
-    prefetch_tmap(&p.tx);
-    prefetch_tmap(&p.tx_row);
-    prefetch_tmap(&p.td);
-    prefetch_tmap(&p.td_row);
+    if (!GATHER) prefetch_tmap(&p.tx[0]);
+    prefetch_tmap(&p.td[0]);
     prefetch_tmap(&p.tdw);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(c.full0 + 8 * s, GATHER ? 3 : 1);   // the leader's TMA warp, and a relay of each CTA
@@ -160,8 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
           const int r0 = r + h * BK, v = min(BK, end - r0);
           if (v <= 0) break;                    // not multiplied either
           const uint32_t off = st * OP_STAGE + h * HALF;
-          if (!GATHER) load_operand(smem_u32(c.sA + off), &p.tx, &p.tx_row, p.x_rows, a0, r0, v, fb, lane);
-          load_operand(smem_u32(c.sB + off), &p.td, &p.td_row, p.R, b0, r0, v, fb, lane);
+          if (!GATHER) load_operand(smem_u32(c.sA + off), p.tx, p.x_rows, a0, r0, v, fb, lane);
+          load_operand(smem_u32(c.sB + off), p.td, p.R, b0, r0, v, fb, lane);
         }
         ++loaded;
         if (++st == STAGES) { st = 0; phase ^= 1u; }
@@ -435,9 +441,10 @@ tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s) {
   if (units > INT32_MAX / 2) return fail(TP_ESHAPE, "too many tiles");
   p.units = static_cast<int>(units);
   p.out_f32 = g.out_f32;
-  if (!encode_bf16_2d(&p.tx, g.x, g.k, g.x_rows, g.k, 64, 64) || !encode_bf16_2d(&p.tx_row, g.x, g.k, g.x_rows, g.k, 64, 1) ||
-      !encode_bf16_2d(&p.td, g.dy, g.n, g.R, g.n, 64, 64) || !encode_bf16_2d(&p.td_row, g.dy, g.n, g.R, g.n, 64, 1))
-    return fail(TP_ECUDA, "cannot encode the TMA descriptors");
+  for (int i = 0; i < 7; ++i)
+    if ((g.row_index == nullptr && !encode_bf16_2d(&p.tx[i], g.x, g.k, g.x_rows, g.k, 64, 64 >> i)) ||
+        !encode_bf16_2d(&p.td[i], g.dy, g.n, g.R, g.n, 64, 64 >> i))
+      return fail(TP_ECUDA, "cannot encode the TMA descriptors");
   if (!encode_out_3d(&p.tdw, g.dw, g.out_f32, g.n, g.k, g.E)) return fail(TP_ECUDA, "cannot encode the TMA descriptor of dW");
   p.status = status_word();
   p.budget = wait_budget();
