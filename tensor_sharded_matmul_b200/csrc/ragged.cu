@@ -15,8 +15,9 @@
 //
 // Adapters (y = x W + s_a (x A_a) B_a): the rows are the tokens sorted by adapter, v = s_a x A_a comes
 // from a first product over the adapters' segments, and v B_a is accumulated into the same TMEM tile
-// as further k-blocks: 16 ranks of one adapter are one MMA step, whose x-side operand holds v for the
-// tokens of that adapter and zeros for the others. v is held in binary32 and enters as two bf16
+// as further k-blocks: 16 ranks of one adapter are one MMA step over the (sixteens of) rows that it owns, with
+// zeros for other rows among them. The second product is launched as a dependent of the first: it
+// multiplies x by W while v is still being made. v is held in binary32 and enters as two bf16
 // numbers (v = hi + lo, |v - hi - lo| <= 2^-16 |v|), so that nothing is rounded to bf16 between the two
 // products.
 #include <cstring>
@@ -33,30 +34,31 @@ constexpr int STAGES = 4;
 constexpr uint32_t W_STAGE = BM * BK * 2;     // 16 KiB
 constexpr uint32_t W_BOX = 64 * BK * 2;       // 64 columns x 64 k: 8 KiB
 constexpr int THREADS = 192;                  // loads, MMA, 4 warps that read TMEM
+constexpr int COPY_FROM = 17;                 // rows of a tile from which cp.async fetches x
 constexpr int STG_LD = BM + 4;                // floats between rows of the staged output tile
 constexpr int MAX_SEGS = TP_MAX_EXPERTS;
 
-template <int NT>
-constexpr size_t smem_bytes() {
-  return 1024 + STAGES * (W_STAGE + NT * BK * 2) + (2 * STAGES + 4) * 8 + 16 + (MAX_SEGS + 4) * 4 + 2 * NT * 4;
-}
+constexpr int NT = 64;                        // rows per tile, at most
+constexpr uint32_t X_STAGE = NT * BK * 2;     // 8 KiB
+constexpr uint32_t TMEM_COLS = NT;
+static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM is allocated in powers of two from 32 columns");
+static_assert(STAGES % 2 == 0, "the indices behind the 3 * STAGES + 4 barriers start on 16 bytes");
+constexpr size_t SMEM = 1024 + STAGES * (W_STAGE + X_STAGE) + (3 * STAGES + 4) * 8 + 16 + (MAX_SEGS + 4) * 4 + 2 * NT * 4;
 
-template <int NT, bool SWIGLU, bool LORA>
+template <bool SWIGLU, bool LORA>
 __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__ RaggedParams p) {
   static_assert(NT * STG_LD * 4 <= STAGES * (W_STAGE + NT * BK * 2), "the staged output tile reuses the operand stages");
-  constexpr uint32_t X_STAGE = NT * BK * 2;
-  constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_w = smem;
   uint8_t* s_x = smem + STAGES * W_STAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_x + STAGES * X_STAGE);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES;
-  const uint32_t accf = empty0 + 8 * STAGES, drain = accf + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, rows0 = empty0 + 8 * STAGES;
+  const uint32_t accf = rows0 + 8 * STAGES, drain = accf + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int* s_count = reinterpret_cast<int*>(tmem_slot + 2);            // adapters of this tile
-  int* s_off = reinterpret_cast<int*>(bars + 2 * STAGES + 4) + 4;  // 16-byte aligned
+  int* s_off = reinterpret_cast<int*>(bars + 3 * STAGES + 4) + 4;  // 16-byte aligned
   int* s_idx = s_off + MAX_SEGS + 4;
   int* s_list = s_idx + NT;
   const int warp = threadIdx.x / 32;
@@ -70,12 +72,14 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
+      mbar_init(rows0 + 8 * s, 128);
     }
     mbar_init(accf, 1);
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
+  if (p.starts_next) launch_dependents();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
@@ -113,10 +117,29 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   }
   constexpr int TILE_N = SWIGLU ? BM / 2 : BM;       // output columns per tile
   const int n0 = ct * TILE_N;
-
-  if (live) {
+  // this CTA's share of the contraction: k-blocks of x (k-blocks of adapters follow)
+  const int kb0 = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split) : 0;
+  const int base = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split) - kb0 : 0;
+  // Few rows of x come by TMA, four a load; from 17 on warps 2..5 copy them.
+  const bool copy = live && valid >= COPY_FROM;
+  const int groups = copy || !live ? 0 : (valid + 3) / 4;
+  auto load_w = [&](int step) {
+    const uint32_t fb = full0 + 8 * (step % STAGES), dst = smem_u32(s_w + (step % STAGES) * W_STAGE);
+    const int k0 = (kb0 + step) * BK;
+    mbar_arrive_expect_tx(fb, W_STAGE + groups * 512u);
+    if (p.w_km) {
+      tma_load_3d(dst, &p.tw, k0, n0, e, fb);
+    } else {
+      tma_load_3d(dst, &p.tw, n0, k0, e, fb);
+      tma_load_3d(dst + W_BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? n0 : n0 + 64, k0, e, fb);
+    }
+  };
+  const int ahead = min(base, STAGES);               // W of the first stages is on its way before the rows are known
+  if (warp == 0 && lane == 0)
+    for (int step = 0; step < ahead; ++step) load_w(step);
+  if (live && warp != 0) {
     // x's row of every row of the tile; -1: the index lies outside x (the row reads as zeros)
-    for (int j = threadIdx.x; j < ((valid + 3) & ~3); j += THREADS) {
+    for (int j = threadIdx.x - 32; j < ((valid + 3) & ~3); j += THREADS - 32) {
       const int i = i0 + min(j, valid - 1);
       const int r = p.row_index != nullptr ? __ldg(p.row_index + i) : i;
       s_idx[j] = r >= 0 && r < p.x_rows ? r : -1;
@@ -138,16 +161,15 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
 
   const int per_adapter = LORA ? (p.rank + 15) / 16 : 1;            // 16-rank steps of one adapter
   const int chunks = LORA && live ? *s_count * per_adapter : 0;
-  const int total_kb = p.num_kb + (chunks + 1) / 2;                 // two adapter steps per k-block
-  const int kb0 = live ? static_cast<int>(static_cast<int64_t>(total_kb) * rank / p.split) : 0;
-  const int kb1 = live ? static_cast<int>(static_cast<int64_t>(total_kb) * (rank + 1) / p.split) : 0;
+  const int extra = (chunks + 1) / 2;                               // k-blocks of two adapter steps
+  const int x0 = extra * rank / p.split;
+  const int steps = live ? base + extra * (rank + 1) / p.split - x0 : 0;
   const int n_mma = live ? (valid + 15) & ~15 : 16;
   int loaded = 0;                                                   // warp 0: k-blocks loaded
   bool mma_issued = false;
 
   if (warp == 0 && live) {
-    const int groups = (valid + 3) / 4;                             // four rows of x per load
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int step = 0; step < steps; ++step) {
       const int st = loaded % STAGES;
       bool ok = mbar_wait_bounded(empty0 + 8 * st, ((loaded / STAGES) & 1) ^ 1, p.budget, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -158,46 +180,18 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
       }
       const uint32_t fb = full0 + 8 * st;
       const uint32_t w_dst = smem_u32(s_w + st * W_STAGE), x_dst = smem_u32(s_x + st * X_STAGE);
-      if (!LORA || kb < p.num_kb) {
-        const int k0 = kb * BK;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(fb, W_STAGE + groups * 512u);
-          if (p.w_km) {
-            tma_load_3d(w_dst, &p.tw, k0, n0, e, fb);
-          } else {
-            tma_load_3d(w_dst, &p.tw, n0, k0, e, fb);
-            tma_load_3d(w_dst + W_BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? n0 : n0 + 64, k0, e, fb);
-          }
-        }
+      if (!LORA || step < base) {
+        const int k0 = (kb0 + step) * BK;
+        if (lane == 0 && step >= ahead) load_w(step);
         __syncwarp();
         for (int g = lane; g < groups; g += 32) {
           const int4 r = *reinterpret_cast<const int4*>(s_idx + 4 * g);
           tma_gather4(x_dst + 512u * g, &p.tx, k0, max(r.x, 0), max(r.y, 0), max(r.z, 0), max(r.w, 0), fb);
         }
       } else {
-        // two 16-rank steps: B's rows by TMA, v of the tokens that the adapter owns by this warp
-        const int c0 = 2 * (kb - p.num_kb);
-        for (int it = lane; it < n_mma * 4; it += 32) {
-          const int row = it >> 2, ch = (it >> 1) & 1, sub = it & 1;
-          const int c = c0 + ch;
-          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-          if (c < chunks && row < valid) {
-            const int a = s_list[c / per_adapter];
-            const int r0 = (c % per_adapter) * 16 + sub * 8;
-            const int i = i0 + row;
-            if (i >= s_off[a] && i < s_off[a + 1] && r0 < p.rank) {
-              split_bf8(p.v + static_cast<int64_t>(i) * p.rank + r0, hi, lo);
-            }
-          }
-          uint8_t* line = s_x + st * X_STAGE + row * 128;
-          const int piece = 2 * ch + sub;                  // hi in pieces 0..3, lo in 4..7
-          *reinterpret_cast<uint4*>(line + ((piece ^ (row & 7)) << 4)) = hi;
-          *reinterpret_cast<uint4*>(line + (((piece + 4) ^ (row & 7)) << 4)) = lo;
-        }
-        fence_proxy_async();
-        __syncwarp();
+        // two 16-rank steps: B's rows (v of the tokens comes from warps 2..5)
         if (lane == 0) {
-          const int nch = min(2, chunks - c0);
+          const int c0 = 2 * (x0 + step - base), nch = min(2, chunks - c0);
           mbar_arrive_expect_tx(fb, nch * 4096u);
           for (int ch = 0; ch < nch; ++ch) {
             const int a = s_list[(c0 + ch) / per_adapter];
@@ -213,28 +207,42 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   } else if (warp == 1 && lane == 0 && live) {
     const uint32_t idesc = idesc_bf16_f32(BM, n_mma, !p.w_km, false);
     int done = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++done) {
+    uint32_t rows_phase = 0;                               // one bit per stage
+    for (int step = 0; step < steps; ++step, ++done) {
       const int st = done % STAGES;
       if (!mbar_wait_bounded(full0 + 8 * st, (done / STAGES) & 1, p.budget, abort_flag)) {
         if (!*abort_flag) record_timeout(p.status, WAIT_MMA_FULL);
         *abort_flag = 1u;
         break;
       }
+      if (copy || (LORA && step >= base)) {                // the rows that warps 2..5 brought
+        if (!mbar_wait_bounded(rows0 + 8 * st, (rows_phase >> st) & 1, p.budget, abort_flag)) {
+          if (!*abort_flag) record_timeout(p.status, WAIT_MMA_FULL);
+          *abort_flag = 1u;
+          break;
+        }
+        rows_phase ^= 1u << st;
+        fence_proxy_async();
+      }
       tc_fence_after();
       const uint32_t w_base = smem_u32(s_w + st * W_STAGE), x_base = smem_u32(s_x + st * X_STAGE);
-      if (!LORA || kb < p.num_kb) {
+      if (!LORA || step < base) {
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k) {
           const uint64_t ad = p.w_km ? smem_desc_sw128(w_base + 32u * k, 16u, 1024u)
                                      : smem_desc_sw128(w_base + 2048u * k, W_BOX, 1024u);
-          umma_bf16(tmem_base, ad, smem_desc_sw128(x_base + 32u * k, 16u, 1024u), idesc, (kb != kb0 || k != 0) ? 1u : 0u);
+          umma_bf16(tmem_base, ad, smem_desc_sw128(x_base + 32u * k, 16u, 1024u), idesc, (step | k) != 0 ? 1u : 0u);
         }
       } else {
-        const int nch = min(2, chunks - 2 * (kb - p.num_kb));
-        for (int q = 0; q < 2 * nch; ++q) {                // hi and lo of each step against the same rows of B
-          const int ch = q >> 1, half = q & 1;
-          umma_bf16(tmem_base, smem_desc_sw128(w_base + 2048u * ch, W_BOX, 1024u),
-                    smem_desc_sw128(x_base + 32u * (ch + 2 * half), 16u, 1024u), idesc, (kb != kb0 || q != 0) ? 1u : 0u);
+        // hi and lo of each step against the same rows of B, for the adapter's rows alone (in sixteens)
+        const int c0 = 2 * (x0 + step - base);
+        for (int ch = 0; ch < min(2, chunks - c0); ++ch) {
+          const int a = s_list[(c0 + ch) / per_adapter];
+          const int first = (max(s_off[a], i0) - i0) & ~15, last = (min(s_off[a + 1], i0 + valid) - i0 + 15) & ~15;
+          const uint32_t id = idesc_bf16_f32(BM, last - first, true, false);
+          const uint64_t ad = smem_desc_sw128(w_base + 2048u * ch, W_BOX, 1024u);
+          for (int half = 0; half < 2; ++half)
+            umma_bf16(tmem_base + first, ad, smem_desc_sw128(x_base + first * 128u + 32u * (ch + 2 * half), 16u, 1024u), id, 1u);
         }
       }
       mma_issued = true;
@@ -242,6 +250,62 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
     }
     umma_commit(accf);
   } else if (warp >= 2 && live) {
+    const int tid = threadIdx.x - 64;
+    const int piece = tid & 7, r0 = tid >> 3;
+    if (copy || (LORA && steps > base)) {
+      int idx[NT / 16];
+#pragma unroll
+      for (int i = 0; i < NT / 16; ++i) idx[i] = r0 + 16 * i < valid ? s_idx[r0 + 16 * i] : -2;
+      for (int step = copy ? 0 : base; step < steps; ++step) {
+        const int st = step % STAGES;
+        uint4 hi[2], lo[2];
+        const int c0 = 2 * (x0 + step - base);
+        if (LORA && step >= base) {                        // loaded before the slot is waited for
+          if (step == base) wait_prerequisites();          // v is the kernel before's
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            hi[ch] = lo[ch] = make_uint4(0, 0, 0, 0);
+            if (c0 + ch >= chunks) continue;
+            const int a = s_list[(c0 + ch) / per_adapter];
+            const int i = i0 + (tid >> 1), k = ((c0 + ch) % per_adapter) * 16 + (tid & 1) * 8;
+            if (i < i0 + valid && i >= s_off[a] && i < s_off[a + 1] && k < p.rank)
+              split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k, hi[ch], lo[ch]);
+          }
+        }
+        bool ok = mbar_wait_bounded(empty0 + 8 * st, ((step / STAGES) & 1) ^ 1, p.budget, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (!*abort_flag) record_timeout(p.status, WAIT_PRODUCER_EMPTY);
+          *abort_flag = 1u;
+          break;
+        }
+        const uint32_t x_dst = smem_u32(s_x + st * X_STAGE);
+        if (!LORA || step < base) {
+          const int k = (kb0 + step) * BK + piece * 8;
+#pragma unroll
+          for (int i = 0; i < NT / 16; ++i) {
+            const int row = r0 + 16 * i;
+            if (idx[i] != -2) {
+              const bool in = idx[i] >= 0 && k < p.K;
+              cp_async16(x_dst + row * 128 + ((piece ^ (row & 7)) << 4),
+                         in ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x, in ? 16u : 0u);
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(rows0 + 8 * st) : "memory");
+        } else {
+          const int row = tid >> 1;
+          uint8_t* line = s_x + st * X_STAGE + row * 128;
+          for (int ch = 0; ch < 2; ++ch) {                 // hi in pieces 0..3, lo in 4..7
+            const int at = 2 * ch + (tid & 1);
+            *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) = hi[ch];
+            *reinterpret_cast<uint4*>(line + (((at + 4) ^ (row & 7)) << 4)) = lo[ch];
+          }
+          mbar_arrive(rows0 + 8 * st);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    if (LORA) wait_prerequisites();                        // completes after the kernel before, always
     // TMEM lane = column of W, TMEM column = row of the tile -> staged [row][column] in shared memory
     // (the operand stages are free: the commit says that every MMA, and so every load, is done)
     if (!mbar_wait_bounded(accf, 0, p.budget, abort_flag)) {
@@ -328,31 +392,32 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <int NT, bool SWIGLU, bool LORA>
+template <bool SWIGLU, bool LORA>
 tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
   static int configured_for[64] = {};
-  constexpr size_t smem = smem_bytes<NT>();
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
   if (dev < 0 || dev >= 64 || !configured_for[dev]) {
-    if (cudaFuncSetAttribute(ragged_kernel<NT, SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", smem);
+    if (cudaFuncSetAttribute(ragged_kernel<SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SMEM)) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
     if (dev >= 0 && dev < 64) configured_for[dev] = 1;
   }
   if (units * p.split > INT32_MAX) return fail(TP_ESHAPE, "too many tiles");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(p.split);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;    // adapters: starts beside the first product
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<NT, SWIGLU, LORA>, p);
+  cfg.numAttrs = LORA ? 2 : 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<SWIGLU, LORA>, p);
   if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_kernel: %s", cudaGetErrorString(err));
   return check_launch("ragged_kernel");
 }
@@ -381,7 +446,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
   p.num_kb = static_cast<int>((g.K + BK - 1) / BK);
   p.L = g.L; p.rank = g.rank;
-  p.act = g.act; p.w_km = g.w_km; p.out_f32 = g.out_f32; p.backward = g.backward; p.scatter = lora;
+  p.act = g.act; p.w_km = g.w_km; p.out_f32 = g.out_f32; p.backward = g.backward; p.starts_next = g.starts_next;
   p.status = status_word();
   p.budget = wait_budget();
   if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");
@@ -390,18 +455,15 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
   const bool narrow = g.R <= 64 * segs;
   if (!narrow) return ragged_pairs(p, swiglu, lora, lora ? (g.R + 255) / 256 : g.R / 256 + segs, s);
-  const int nt = narrow ? 64 : 256;
-  const int64_t row_tiles = lora ? (g.R + nt - 1) / nt : g.R / nt + segs;
-  const int64_t units = row_tiles * p.tiles_n * (lora ? g.E : 1);
+  const int64_t units = (lora ? 1 : g.R / NT + segs) * p.tiles_n * (lora ? g.E : 1);
+  // Two CTAs fit an SM: split the contraction (in shares of four k-blocks at least) by powers of two while
+  // all CTAs find room at once. 50 MB of W for one token: 35 us unsplit, 23 by two, 20 by four, 27 by
+  // eight (more than fit), 29 by six (clusters of six pack badly).
+  const int64_t room = 2ll * sm_count();
   p.split = 1;
-  const int sms = sm_count();
-  while (p.split < 8 && units * p.split < sms && p.num_kb >= 8 * p.split) p.split *= 2;
-  if (narrow) {
-    if (lora) return launch_ragged<64, false, true>(p, units, s);
-    return swiglu ? launch_ragged<64, true, false>(p, units, s) : launch_ragged<64, false, false>(p, units, s);
-  }
-  if (lora) return launch_ragged<256, false, true>(p, units, s);
-  return swiglu ? launch_ragged<256, true, false>(p, units, s) : launch_ragged<256, false, false>(p, units, s);
+  while (p.split < 8 && units * p.split * 2 <= room && p.num_kb >= 8 * p.split) p.split *= 2;
+  if (lora) return launch_ragged<false, true>(p, units, s);
+  return swiglu ? launch_ragged<true, false>(p, units, s) : launch_ragged<false, false>(p, units, s);
 }
 
 }  // namespace tpx

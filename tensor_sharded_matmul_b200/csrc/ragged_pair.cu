@@ -40,6 +40,7 @@ constexpr int LOADERS = 8, RELAYS = 2;              // warps that fetch gathered
 constexpr int EPI = 8;                              // epilogue warps: two groups of four
 constexpr int LOAD0 = 2 + EPI, RELAY0 = LOAD0 + LOADERS;   // first warps; before them TMA, MMA, epilogue
 constexpr int THREADS = 32 * (RELAY0 + RELAYS);
+static_assert(32 * LOADERS == 2 * 128, "two threads build one row of adapter values");
 constexpr int STG_LD = 128 + 4;                     // floats between staged rows
 constexpr int CHUNK = 16;                           // rows that a group turns around at a time
 constexpr uint32_t STAGING = 2 * CHUNK * STG_LD * 4;
@@ -179,6 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
+  if (p.starts_next) launch_dependents();
   const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
   tc_fence_before();
@@ -400,6 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x - 32 * LOAD0;
     constexpr int STEP = LOADERS * 4;                  // rows of one pass
     const int piece = tid & 7, r0 = tid >> 3;
+    const int v_row = tid >> 1;                        // adapters: two threads build one row of 32 values
+    bool waited = false;
     int st = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -422,6 +426,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int total_kb = p.num_kb + (chunks + 1) / 2;
       int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
       for (int kb = 0; kb < total_kb; kb += KB) {
+        // a stage that holds rows of v: they are loaded before its slot is waited for
+        const bool extra = LORA && kb + KB > p.num_kb && total_kb > p.num_kb;
+        uint4 hi[2 * KB], lo[2 * KB];
+        if (extra) {
+          if (!waited) wait_prerequisites();           // v is the kernel before's
+          waited = true;
+#pragma unroll
+          for (int i = 0; i < 2 * KB; ++i) {
+            hi[i] = lo[i] = make_uint4(0, 0, 0, 0);
+            const int chunk = 2 * (kb - p.num_kb) + i;
+            if (chunk < 0 || chunk >= chunks) continue;
+            const int row = t.i0 + half0 + v_row, k0 = q * 16 + (tid & 1) * 8;
+            if (v_row < mine && row >= s_off[a] && row < s_off[a + 1] && k0 < p.rank)
+              split_bf8(p.v + static_cast<int64_t>(row) * p.rank + k0, hi[i], lo[i]);
+            if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+          }
+        }
         ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
         if (!ok) break;
 #pragma unroll
@@ -438,25 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                            in ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x, in ? 16u : 0u);
               }
             }
-          } else if (LORA && kb + h < total_kb) {
-            const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
-            for (int ch = 0; ch < nch; ++ch) {
-              for (int it = tid; it < 2 * nh; it += 32 * LOADERS) {
-                const int row = it >> 1, sub = it & 1;
-                const int i = t.i0 + half0 + row, k0 = q * 16 + sub * 8;
-                uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-                if (row < mine && i >= s_off[a] && i < s_off[a + 1] && k0 < p.rank)
-                  split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k0, hi, lo);
-                uint8_t* line = x + row * 128;
-                const int pc = 2 * ch + sub;
-                *reinterpret_cast<uint4*>(line + ((pc ^ (row & 7)) << 4)) = hi;
-                *reinterpret_cast<uint4*>(line + (((pc + 4) ^ (row & 7)) << 4)) = lo;
-              }
-              if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+          } else if (extra && v_row < nh) {
+            uint8_t* line = x + v_row * 128;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              const int pc = 2 * ch + (tid & 1);
+              *reinterpret_cast<uint4*>(line + ((pc ^ (v_row & 7)) << 4)) = hi[2 * h + ch];
+              *reinterpret_cast<uint4*>(line + (((pc + 4) ^ (v_row & 7)) << 4)) = lo[2 * h + ch];
             }
           }
         }
-        if (LORA && kb + KB > p.num_kb && total_kb > p.num_kb) {   // holds rows of v, written by ordinary stores
+        if (extra) {
           asm volatile("cp.async.wait_all;" ::: "memory");
           mbar_arrive(c.rows0 + 8 * st);
         } else {
@@ -466,6 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (LORA) wait_prerequisites();                    // completes after the kernel before, always
   } else if (gather) {
     // Relays, the stages in turn: what the loaders wrote is ordered before the tensor cores' reads and
     // passed on to the leader's barrier. (The loaders cannot do it themselves: a release to the other CTA
@@ -530,7 +544,18 @@ tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
   const int sms = sm_count();
   int grid = 2 * units < sms ? static_cast<int>(2 * units) : (sms & ~1);
   if (grid < 2) grid = 2;
-  ragged_pair_kernel<SWIGLU, LORA><<<grid, THREADS, SMEM, s>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];                                        // adapters: starts beside the first product
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = LORA ? 1 : 0;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_pair_kernel<SWIGLU, LORA>, p);
+  if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_pair_kernel: %s", cudaGetErrorString(err));
   return check_launch("ragged_pair_kernel");
 }
 
