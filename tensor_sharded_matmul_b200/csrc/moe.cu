@@ -22,7 +22,8 @@ namespace {
 
 constexpr int TB = 64;                // tokens per block of the router and the sort
 constexpr int WORDS = TB / 32;
-constexpr int ROUTE_THREADS = 512;
+template <int VPL>
+constexpr int ROUTE_THREADS = VPL <= 8 ? 1024 : 512;      // registers of a long list
 
 // Order-preserving integer of a float (no NaN): a < b <=> key(a) < key(b). key(-inf) = 0x007fffff.
 constexpr uint32_t KEY_MASKED = 0x007fffffu;
@@ -62,18 +63,9 @@ struct SortParams {
   int32_t* offsets;          // [E + 1]
   int32_t* row_token;        // [N * k]
   int32_t* counts;           // [E + rest][blocks], then the buckets' totals [E + rest]
+  int32_t* rank;             // [N][k]: places inside the block (slot itself where there is one)
 };
 
-// Sets the bits of this block's entries; `bits`: [buckets][WORDS], cleared before.
-__device__ __forceinline__ void mark_entries(const SortParams& p, uint32_t* bits, int64_t n0) {
-  for (int i = threadIdx.x; i < TB * p.k; i += blockDim.x) {
-    const int t = i / p.k;
-    if (n0 + t >= p.N) break;
-    int e = p.expert[(n0 + t) * p.k + (i - t * p.k)];
-    if (p.rest && (e < 0 || e >= p.E)) e = p.E;
-    if (e >= 0) atomicOr(bits + e * WORDS + t / 32, 1u << (t % 32));
-  }
-}
 __device__ __forceinline__ void clear_bits(uint32_t* bits, int buckets) {
   for (int i = threadIdx.x; i < buckets * WORDS; i += blockDim.x) bits[i] = 0u;
 }
@@ -103,113 +95,158 @@ __device__ __forceinline__ void scan_in_place(int* v, int n, int lane) {
   __syncwarp();
 }
 
-// Writes slot and row_token of this block's entries. start[e]: the block's first row in bucket e.
-__device__ __forceinline__ void place_entries(const SortParams& p, const uint32_t* bits, const int* start, int64_t n0) {
-  for (int i = threadIdx.x; i < TB * p.k; i += blockDim.x) {
-    const int t = i / p.k;
-    if (n0 + t >= p.N) break;
-    const int64_t at = (n0 + t) * p.k + (i - t * p.k);
-    int e = p.expert[at];
-    if (p.rest && (e < 0 || e >= p.E)) e = p.E;
-    int row = -1;
-    if (e >= 0) {
-      row = start[e] + __popc(bits[e * WORDS + t / 32] & ((1u << (t % 32)) - 1u));
-      for (int w = 0; w < t / 32; ++w) row += __popc(bits[e * WORDS + w]);
-      p.row_token[row] = static_cast<int32_t>(n0 + t);
+// The place of entry (t, e) among the block's entries of bucket e.
+__device__ __forceinline__ int rank_in_block(const uint32_t* bits, int e, int t) {
+  int r = __popc(bits[e * WORDS + t / 32] & ((1u << (t % 32)) - 1u));
+  for (int w = 0; w < t / 32; ++w) r += __popc(bits[e * WORDS + w]);
+  return r;
+}
+
+// This block's entries: `pick` [tokens][k] their buckets (-1: none), `bits` set, `start` room for the buckets
+// and one more. A batch of one block is finished; otherwise the counts go to p.counts and the ranks to
+// p.rank, for sort_scan_kernel and sort_place_kernel.
+__device__ __forceinline__ void place_block(const SortParams& p, const uint32_t* bits, int* start, const int* pick, int64_t n0) {
+  const int buckets = p.E + p.rest;
+  const int entries = static_cast<int>(p.N - n0 < TB ? p.N - n0 : TB) * p.k;
+  if (p.blocks == 1) {
+    for (int e = threadIdx.x; e < buckets; e += blockDim.x) start[e] = bucket_count(bits, e);
+    __syncthreads();
+    if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
+  } else {
+    for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+      p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = bucket_count(bits, e);
+  }
+  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
+    const int e = pick[i], t = i / p.k;
+    int row = e >= 0 ? rank_in_block(bits, e, t) : -1;
+    if (p.blocks == 1) {
+      if (e >= 0) {
+        row += start[e];
+        p.row_token[row] = static_cast<int32_t>(n0 + t);
+      }
+      if (p.slot != nullptr) p.slot[n0 * p.k + i] = row;
+    } else {
+      p.rank[n0 * p.k + i] = row;
     }
-    if (p.slot != nullptr) p.slot[at] = row;
   }
 }
 
-// One block holds the whole batch: offsets and places from its bitmap alone.
-__device__ __forceinline__ void place_alone(const SortParams& p, const uint32_t* bits, int* start) {
-  const int buckets = p.E + p.rest;
-  for (int e = threadIdx.x; e < buckets; e += blockDim.x) start[e] = bucket_count(bits, e);
-  __syncthreads();
-  if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
-  __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
-  place_entries(p, bits, start, 0);
+// A lane's keys in descending order, equal keys by ascending expert (an odd-even network; the lane's
+// experts ascend with i, so equal neighbours need no exchange).
+template <int VPL>
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[VPL], int (&at)[VPL]) {
+#pragma unroll
+  for (int r = 0; r < VPL; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < VPL; i += 2) {
+      const bool swap = key[i + 1] > key[i];
+      const uint32_t k = key[i];
+      const int a = at[i];
+      key[i] = swap ? key[i + 1] : k;
+      key[i + 1] = swap ? k : key[i + 1];
+      at[i] = swap ? at[i + 1] : a;
+      at[i + 1] = swap ? a : at[i + 1];
+    }
 }
 
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const void* __restrict__ logits, int gate,
+__global__ void __launch_bounds__(ROUTE_THREADS<VPL>) route_kernel(const void* __restrict__ logits, int gate,
                                                               float* __restrict__ weight, SortParams p) {
   extern __shared__ int s_dyn[];
   uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);         // [E][WORDS]
   int* start = s_dyn + p.E * WORDS;                            // [E + 1]
+  int* s_pick = start + p.E + 1;                               // [TB][k]: the block's choices
+  constexpr bool SORTED = VPL <= 8;                            // a longer list is searched each time
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
   clear_bits(bits, p.E);
   __syncthreads();
-  for (int t = warp; t < TB && n0 + t < p.N; t += ROUTE_THREADS / 32) {
+  for (int t = warp; t < TB && n0 + t < p.N; t += ROUTE_THREADS<VPL> / 32) {
     const int64_t n = n0 + t;
     uint32_t key[VPL];
-    float m = -INFINITY;
+    int at[VPL];                                               // the expert of each key
     float v[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
       v[i] = e < p.E ? load_logit<BF16>(logits, n * p.E + e) : -INFINITY;
       key[i] = key_of(v[i]);
-      m = fmaxf(m, v[i]);
+      at[i] = e;
     }
-    m = warp_max(m);
-    float total = 0.0f;
-    if (gate == TP_GATE_SOFTMAX && m > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) total += expf(v[i] - m);
-      total = warp_sum(total);
-    }
+    if constexpr (SORTED) sort_lane(key, at);
     int my_e = -1;
-    float my_w = 0.0f;                                         // lane j: the j-th choice
+    uint32_t my_key = KEY_MASKED, first = KEY_MASKED;          // lane j: the j-th choice; all: the first
     for (int j = 0; j < p.k; ++j) {
-      uint32_t best = 0;
-      int at = 0;
+      uint32_t best = key[0];
+      int best_e = at[0];
+      if constexpr (!SORTED) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) { best = key[i]; at = i; }
+        for (int i = 1; i < VPL; ++i)
+          if (key[i] > best) { best = key[i]; best_e = at[i]; }
+      }
       const uint32_t top = __reduce_max_sync(0xffffffffu, best);
       if (top <= KEY_MASKED) break;                            // no expert left
-      const unsigned e = __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(lane + 32 * at) : 0xffffffffu);
+      const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(best_e) : 0xffffffffu));
+      const bool mine = best_e == e;                           // this lane's is taken
+      if constexpr (SORTED) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i == static_cast<int>(e)) key[i] = 0;
+        for (int i = 0; i + 1 < VPL; ++i) {
+          key[i] = mine ? key[i + 1] : key[i];
+          at[i] = mine ? at[i + 1] : at[i];
+        }
+        key[VPL - 1] = mine ? 0u : key[VPL - 1];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (mine && at[i] == best_e) key[i] = 0;
+      }
+      if (j == 0) first = top;
       if (lane == j) {
-        my_e = static_cast<int>(e);
-        my_w = expf(of_key(top) - m);
+        my_e = e;
+        my_key = top;
       }
     }
-    if (gate == TP_GATE_TOPK) total = warp_sum(my_w);
+    const float m = of_key(first);
+    const float my_w = my_e >= 0 ? expf(of_key(my_key) - m) : 0.0f;
+    float total = my_w;
+    if (gate == TP_GATE_SOFTMAX) {
+      total = 0.0f;
+      if (first > KEY_MASKED) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) total += expf(v[i] - m);
+      }
+    }
+    total = warp_sum(total);
     if (lane < p.k) {
       p.expert[n * p.k + lane] = my_e;
       weight[n * p.k + lane] = my_e >= 0 ? my_w / total : 0.0f;
+      s_pick[t * p.k + lane] = my_e;
       if (my_e >= 0) atomicOr(bits + my_e * WORDS + t / 32, 1u << (t % 32));
     }
   }
   __syncthreads();
-  if (p.blocks == 1) {
-    place_alone(p, bits, start);
-  } else {
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-      p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = bucket_count(bits, e);
-  }
+  place_block(p, bits, start, s_pick, n0);
 }
 
 __global__ void __launch_bounds__(256) sort_count_kernel(SortParams p) {
   extern __shared__ int s_dyn[];
-  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);
   const int buckets = p.E + p.rest;
+  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);
+  int* start = s_dyn + buckets * WORDS;
+  int* s_pick = start + buckets + 1;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
   clear_bits(bits, buckets);
   __syncthreads();
-  mark_entries(p, bits, static_cast<int64_t>(blockIdx.x) * TB);
-  __syncthreads();
-  if (p.blocks == 1) {
-    place_alone(p, bits, s_dyn + buckets * WORDS);
-    return;
+  for (int i = threadIdx.x; i < TB * p.k && n0 + i / p.k < p.N; i += blockDim.x) {
+    int e = p.expert[n0 * p.k + i];
+    if (e < 0 || e >= p.E) e = p.rest ? p.E : -1;
+    s_pick[i] = e;
+    if (e >= 0) atomicOr(bits + e * WORDS + i / p.k / 32, 1u << (i / p.k % 32));
   }
-  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
-    p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = bucket_count(bits, e);
+  __syncthreads();
+  place_block(p, bits, start, s_pick, n0);
 }
 
 // One warp per bucket: its blocks' counts become the rows before each block; the total goes behind all.
@@ -236,83 +273,107 @@ __global__ void __launch_bounds__(256) sort_scan_kernel(SortParams p) {
 }
 
 __global__ void __launch_bounds__(256) sort_place_kernel(SortParams p) {
-  extern __shared__ int s_dyn[];
+  extern __shared__ int start[];
   const int buckets = p.E + p.rest;
-  uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);
-  int* start = s_dyn + buckets * WORDS;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
-  clear_bits(bits, buckets);
   for (int e = threadIdx.x; e < buckets; e += blockDim.x)
     start[e] = p.counts[static_cast<int64_t>(buckets) * p.blocks + e];
   __syncthreads();
-  mark_entries(p, bits, n0);
   if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
-  __syncthreads();
-  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
-    start[e] += p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
-  __syncthreads();
-  place_entries(p, bits, start, n0);
+  const int entries = static_cast<int>(p.N - n0 < TB ? p.N - n0 : TB) * p.k;
+  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
+    int e = p.expert[n0 * p.k + i], row = p.rank[n0 * p.k + i];
+    if (row >= 0) {
+      if (e < 0 || e >= p.E) e = p.E;               // the rest, behind all
+      row += start[e] + p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
+      p.row_token[row] = static_cast<int32_t>(n0 + i / p.k);
+    }
+    if (p.slot != nullptr) p.slot[n0 * p.k + i] = row;
+  }
 }
 
 // dlogits of one token per warp. With q the weights' softmax (over all experts, or over the chosen):
-// dl_i = q_i (dw_i - sum_j q_j dw_j), dw zero where not chosen.
+// dl_i = q_i (dw_i - inner), inner = sum_j q_j dw_j, dw zero where not chosen. Every lane writes -q_i inner
+// (TOPK: zero) for its experts; then lane j writes the j-th choice's, from its own copy of that logit. A
+// choice that is named twice has the sum of its dw.
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const void* __restrict__ logits, int64_t N, int E, int k, int gate,
                                                         const int32_t* __restrict__ expert,
-                                                        const float* __restrict__ dweight, void* __restrict__ dlogits) {
+                                                        const float* __restrict__ dweight, void* dlogits) {
   const int lane = threadIdx.x % 32;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
   if (n >= N) return;
-  float v[VPL], d[VPL];
-  bool chosen[VPL];
+  float v[VPL];
+  if (gate == TP_GATE_SOFTMAX) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    v[i] = e < E ? load_logit<BF16>(logits, n * E + e) : -INFINITY;
-    d[i] = 0.0f;
-    chosen[i] = false;
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      v[i] = e < E ? load_logit<BF16>(logits, n * E + e) : -INFINITY;
+    }
   }
-  const int my_e = lane < k ? __ldg(expert + n * k + lane) : -1;
-  const float my_d = lane < k ? __ldg(dweight + n * k + lane) : 0.0f;
+  int my_e = lane < k ? __ldg(expert + n * k + lane) : -1;
+  if (my_e >= E) my_e = -1;
+  float my_d = my_e >= 0 ? __ldg(dweight + n * k + lane) : 0.0f;
+  const float my_v = my_e >= 0 ? load_logit<BF16>(logits, n * E + my_e) : -INFINITY;
+  bool first = my_e >= 0, again = false;           // the lowest lane of equal choices takes the sum of their dw
   for (int j = 0; j < k; ++j) {
-    const int e = __shfl_sync(0xffffffffu, my_e, j);
-    const float g = __shfl_sync(0xffffffffu, my_d, j);
-    if (e < 0) continue;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + 32 * i == e) {
-        d[i] += g;
-        chosen[i] = true;
-      }
+    const bool same = __shfl_sync(0xffffffffu, my_e, j) == my_e && my_e >= 0;
+    if (j < lane && same) first = false;
+    if (j != lane && same) again = true;
   }
-  float m = -INFINITY;
+  if (__any_sync(0xffffffffu, again)) {
+    float sum = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const float d = __shfl_sync(0xffffffffu, my_d, j);
+      if (__shfl_sync(0xffffffffu, my_e, j) == my_e) sum += d;
+    }
+    my_d = sum;
+  }
+  float m = first ? my_v : -INFINITY;
+  if (gate == TP_GATE_SOFTMAX) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (gate == TP_GATE_SOFTMAX || chosen[i]) m = fmaxf(m, v[i]);
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
+  }
   m = warp_max(m);
-  float total = 0.0f, inner = 0.0f;
+  const bool any = m > -INFINITY;
+  const float my_p = first && any ? expf(my_v - m) : 0.0f;
+  float total = my_p;
+  if (gate == TP_GATE_SOFTMAX) {
+    total = 0.0f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    v[i] = m > -INFINITY && (gate == TP_GATE_SOFTMAX || chosen[i]) ? expf(v[i] - m) : 0.0f;
-    total += v[i];
-    inner += v[i] * d[i];
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = any ? expf(v[i] - m) : 0.0f;
+      total += v[i];
+    }
   }
-  total = warp_sum(total);
-  inner = warp_sum(inner);
+  float inner = my_p > 0.0f ? my_p * my_d : 0.0f;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, d);
+    inner += __shfl_xor_sync(0xffffffffu, inner, d);
+  }
   const float r = total > 0.0f ? 1.0f / total : 0.0f;
   inner *= r;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     if (e >= E) continue;
-    const float g = v[i] > 0.0f ? v[i] * r * (d[i] - inner) : 0.0f;
+    const float g = gate == TP_GATE_SOFTMAX && v[i] > 0.0f ? -v[i] * r * inner : 0.0f;
     if constexpr (BF16)
       static_cast<uint16_t*>(dlogits)[n * E + e] = to_bf(g);
     else
       static_cast<float*>(dlogits)[n * E + e] = g;
+  }
+  __syncwarp();
+  if (first && my_p > 0.0f) {
+    const float g = my_p * r * (my_d - inner);
+    if constexpr (BF16)
+      static_cast<uint16_t*>(dlogits)[n * E + my_e] = to_bf(g);
+    else
+      static_cast<float*>(dlogits)[n * E + my_e] = g;
   }
 }
 
@@ -431,12 +492,12 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
 // ------------------------------------------------------------------ launches
 template <bool BF16>
 tp_status launch_route(const void* logits, int gate, float* weight, const SortParams& p, cudaStream_t s) {
-  const size_t smem = (static_cast<size_t>(p.E) * WORDS + p.E + 1) * 4;
+  const size_t smem = (static_cast<size_t>(p.E) * WORDS + p.E + 1 + TB * p.k) * 4;
   const int vpl = (p.E + 31) / 32;
-  if (vpl <= 2) route_kernel<2, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
-  else if (vpl <= 4) route_kernel<4, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
-  else if (vpl <= 8) route_kernel<8, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
-  else route_kernel<32, BF16><<<p.blocks, ROUTE_THREADS, smem, s>>>(logits, gate, weight, p);
+  if (vpl <= 2) route_kernel<2, BF16><<<p.blocks, ROUTE_THREADS<2>, smem, s>>>(logits, gate, weight, p);
+  else if (vpl <= 4) route_kernel<4, BF16><<<p.blocks, ROUTE_THREADS<4>, smem, s>>>(logits, gate, weight, p);
+  else if (vpl <= 8) route_kernel<8, BF16><<<p.blocks, ROUTE_THREADS<8>, smem, s>>>(logits, gate, weight, p);
+  else route_kernel<32, BF16><<<p.blocks, ROUTE_THREADS<32>, smem, s>>>(logits, gate, weight, p);
   return check_launch("route_kernel");
 }
 
@@ -457,7 +518,7 @@ tp_status scan_and_place(const SortParams& p, cudaStream_t s) {
   const int buckets = p.E + p.rest;
   sort_scan_kernel<<<(buckets + 7) / 8, 256, 0, s>>>(p);
   if (tp_status st = check_launch("sort_scan_kernel")) return st;
-  sort_place_kernel<<<p.blocks, 256, (static_cast<size_t>(buckets) * WORDS + buckets + 1) * 4, s>>>(p);
+  sort_place_kernel<<<p.blocks, 256, static_cast<size_t>(buckets + 1) * 4, s>>>(p);
   return check_launch("sort_place_kernel");
 }
 
@@ -544,7 +605,7 @@ tp_status tp_moe_route(const void* logits, tp_dtype dtype, int64_t N, int E, int
     return fail(TP_EALIGN, "pointer not aligned to its elements");
   const size_t need = tp_moe_route_ws_bytes(N, E, k);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
-  SortParams p = {N, E, k, 0, static_cast<int>(sort_blocks(N)), expert, slot, offsets, row_token, static_cast<int32_t*>(ws)};
+  SortParams p = {N, E, k, 0, static_cast<int>(sort_blocks(N)), expert, slot, offsets, row_token, static_cast<int32_t*>(ws), slot};
   if (tp_status st = dtype == TP_BF16 ? launch_route<true>(logits, gate, weight, p, s) : launch_route<false>(logits, gate, weight, p, s))
     return st;
   return p.blocks == 1 ? TP_OK : scan_and_place(p, s);
@@ -717,7 +778,8 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
 
 size_t tp_lora_plan_ws_bytes(int64_t N, int L) {
   if (N <= 0 || L <= 0 || L > TP_MAX_EXPERTS || N > MAX_SIZE) return 0;
-  return sort_ws_bytes(N, L + 1);
+  const size_t counts = sort_ws_bytes(N, L + 1);
+  return counts > 0 ? counts + static_cast<size_t>(N) * 4 : 0;     // and every token's place in its block
 }
 
 tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, int32_t* row_token, void* ws, size_t ws_bytes,
@@ -732,8 +794,8 @@ tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, in
   const size_t need = tp_lora_plan_ws_bytes(N, L);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   SortParams p = {N, L, 1, 1, static_cast<int>(sort_blocks(N)), const_cast<int32_t*>(id), nullptr, offsets, row_token,
-                  static_cast<int32_t*>(ws)};
-  sort_count_kernel<<<p.blocks, 256, (static_cast<size_t>(L + 1) * WORDS + L + 2) * 4, s>>>(p);
+                  static_cast<int32_t*>(ws), static_cast<int32_t*>(ws) + (L + 1) * (sort_blocks(N) + 1)};
+  sort_count_kernel<<<p.blocks, 256, (static_cast<size_t>(L + 1) * WORDS + L + 2 + TB) * 4, s>>>(p);
   if (tp_status st = check_launch("sort_count_kernel")) return st;
   return p.blocks == 1 ? TP_OK : scan_and_place(p, s);
 }
