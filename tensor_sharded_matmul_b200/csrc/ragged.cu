@@ -453,9 +453,13 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   const int tile_n = swiglu ? BM / 2 : BM;
   p.tiles_n = static_cast<int>((g.n + tile_n - 1) / tile_n);
   const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
-  const bool narrow = g.R <= 64 * segs;
-  if (!narrow) return ragged_pairs(p, swiglu, lora, lora ? (g.R + 255) / 256 : g.R / 256 + segs, s);
-  const int64_t units = (lora ? 1 : g.R / NT + segs) * p.tiles_n * (lora ? g.E : 1);
+  // Pairs for segments of more than 64 rows on average, if their tiles (256 rows x 256 columns) keep at
+  // least half of the pairs busy. x A of 4000 tokens, 8 adapters of rank 64, K = 4096: 23 tiles of pairs,
+  // 52 us; 284 CTAs here, 14 us.
+  const int64_t wide_rows = lora ? (g.R + 255) / 256 : g.R / 256 + segs;
+  const int64_t wide_units = wide_rows * ((g.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256)) * (lora ? g.E : 1);
+  if (g.R > 64 * segs && 4 * wide_units >= sm_count()) return ragged_pairs(p, swiglu, lora, wide_rows, s);
+  const int64_t units = (lora ? (g.R + NT - 1) / NT : g.R / NT + segs) * p.tiles_n * (lora ? g.E : 1);
   // Two CTAs fit an SM: split the contraction (in shares of four k-blocks at least) by powers of two while
   // all CTAs find room at once. 50 MB of W for one token: 35 us unsplit, 23 by two, 20 by four, 27 by
   // eight (more than fit), 29 by six (clusters of six pack badly).

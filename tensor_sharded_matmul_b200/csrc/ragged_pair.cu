@@ -5,7 +5,8 @@
 // its N, in steps of 32, each CTA holding half of them. A segment of r rows is cut into ceil(r / 256)
 // tiles of nearly equal height, so that its last tile is not a sliver that streams all of W for a few rows.
 //
-// Per CTA: warp 0 loads W (and, when the rows lie side by side, x) by TMA; warps 10..17 copy gathered rows with
+// Per CTA: warp 0 loads W (and x where its rows lie side by side: a prompt's tokens mostly do when they are
+// sorted by adapter, an expert's tokens do not) by TMA; warps 10..17 copy gathered rows with
 // cp.async and warps 18, 19 hand them over; one thread of the leader's warp 1 issues the MMAs; warps 2..9
 // turn the accumulator's rows around through shared memory and write whole row pieces while the next tile
 // is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
@@ -117,6 +118,22 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
   return t;
 }
 
+// Which groups of 32 rows of one CTA's half (rows first .. first + mine - 1 of the sorted order) lie side by
+// side in x: bit g of the result, and the row of x that group g begins at. Whole warp.
+__device__ __forceinline__ uint32_t runs_of_half(const RaggedParams& p, int first, int mine, int lane, int (&begin)[4]) {
+  int r[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) r[g] = 32 * g + lane < mine ? __ldg(p.row_index + first + 32 * g + lane) : 0;
+  uint32_t runs = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    begin[g] = __shfl_sync(0xffffffffu, r[g], 0);
+    const bool fits = 32 * g + lane >= mine || (r[g] == begin[g] + lane && r[g] >= 0 && r[g] < p.x_rows);
+    if (__all_sync(0xffffffffu, fits) && 32 * g < mine) runs |= 1u << g;
+  }
+  return runs;
+}
+
 // Adapters that own rows of [i0, i0 + valid): how many, and the first from `a` on.
 __device__ __forceinline__ int count_adapters(const int* off, int L, int i0, int valid, int lane) {
   int n = 0;
@@ -159,10 +176,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefetch_tmap(&p.tw);
     if (SWIGLU) prefetch_tmap(&p.tw2);
     if (LORA) prefetch_tmap(&p.tb);
-    if (!gather) {
-      prefetch_tmap(&p.tx_box);
-      prefetch_tmap(&p.tx_box32);
-    }
+    if (!gather) prefetch_tmap(&p.tx_box);
+    prefetch_tmap(&p.tx_box32);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(c.full0 + 8 * s, gather ? 3 : 1);    // the leader's TMA thread, and a relay of each CTA
       mbar_init(c.rows0 + 8 * s, 32 * LOADERS);
@@ -205,6 +220,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int nh = t.n_mma / 2, row0 = t.i0 + static_cast<int>(c.rank) * nh;
       // rows side by side: one box of 128 rows, or (a low tile) as many of 32 as it takes
       const uint32_t x_bytes = gather ? 0u : nh > 96 ? HALF : static_cast<uint32_t>((nh + 31) / 32) * 4096u;
+      // gathered rows: groups that happen to lie side by side come by TMA all the same
+      uint32_t runs = 0;
+      int begin[4] = {0, 0, 0, 0};
+      uint32_t x_both = 2 * x_bytes;                   // of both CTAs
+      if (gather) {
+        const int other = t.i0 + static_cast<int>(c.rank ^ 1u) * nh;
+        x_both = 4096u * __popc(runs_of_half(p, other, min(nh, t.i0 + t.valid - other), lane, begin));
+        runs = runs_of_half(p, row0, min(nh, t.i0 + t.valid - row0), lane, begin);
+        x_both += 4096u * __popc(runs);
+      }
       const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
       const int total_kb = p.num_kb + (chunks + 1) / 2;
       int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
@@ -216,10 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           uint32_t bytes = 0;
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
-            if (kb + h < p.num_kb) bytes += HALF + x_bytes;
-            else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 4096u;
+            if (kb + h < p.num_kb) bytes += 2 * HALF + x_both;
+            else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 8192u;
           }
-          if (c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, 2 * bytes);   // both CTAs load alike
+          if (c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, bytes);   // of both CTAs
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
             const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
@@ -235,6 +260,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               else if (!LORA)
                 for (int b = 0; b < static_cast<int>(x_bytes / 4096u); ++b)
                   tma_load_2d_pair(x + 4096u * b, &p.tx_box32, k0, row0 + 32 * b, fb);
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (runs >> g & 1) tma_load_2d_pair(x + 4096u * g, &p.tx_box32, k0, begin[g], fb);
             } else if (LORA && kb + h < total_kb) {
               const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
               for (int ch = 0; ch < nch; ++ch) {
@@ -412,12 +440,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!t.live) break;
       const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
       const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
+      int begin[4];
+      const uint32_t runs = runs_of_half(p, t.i0 + half0, mine, lane, begin);   // come by TMA
       int idx[128 / STEP];
 #pragma unroll
       for (int i = 0; i < 128 / STEP; ++i) {
         const int row = r0 + STEP * i;
         idx[i] = -2;                                   // no row: left as it is (its column is not read)
-        if (row < mine) {
+        if (row < mine && !(runs >> (row >> 5) & 1)) {
           const int r = __ldg(p.row_index + t.i0 + half0 + row);
           idx[i] = r >= 0 && r < p.x_rows ? r : -1;    // -1: outside x, zeros
         }
