@@ -826,7 +826,6 @@ tp_status tp_lora_linear(const uint16_t* x, int64_t N, int64_t k, int64_t n, int
   std::memset(&g, 0, sizeof(g));
   g.x = x; g.x_rows = N; g.row_index = row_token; g.offsets = offsets; g.R = N; g.E = L; g.K = k; g.n = rank;
   g.w = a; g.act = TP_ACT_NONE; g.y = ws; g.out_f32 = true; g.seg_scale = scale;
-  g.starts_next = true;
   if (tp_status st = ragged_product(g, s)) return st;
   std::memset(&g, 0, sizeof(g));                   // y[r] = x W[r] + v B[r]
   g.x = x; g.x_rows = N; g.row_index = row_token; g.offsets = offsets; g.R = N; g.E = t; g.K = k; g.n = n / t;

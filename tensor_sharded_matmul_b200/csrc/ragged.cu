@@ -40,6 +40,7 @@ constexpr int MAX_SEGS = TP_MAX_EXPERTS;
 
 constexpr int NT = 64;                        // rows per tile, at most
 constexpr uint32_t X_STAGE = NT * BK * 2;     // 8 KiB
+constexpr uint32_t X_BOX = 32 * BK * 2;       // 32 rows
 constexpr uint32_t TMEM_COLS = NT;
 static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM is allocated in powers of two from 32 columns");
 static_assert(STAGES % 2 == 0, "the indices behind the 3 * STAGES + 4 barriers start on 16 bytes");
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
 
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&p.tw);
-    prefetch_tmap(&p.tx);
+    prefetch_tmap(p.row_index != nullptr ? &p.tx : &p.tx_box32);
     if (SWIGLU) prefetch_tmap(&p.tw2);
     if (LORA) prefetch_tmap(&p.tb);
     for (int s = 0; s < STAGES; ++s) {
@@ -79,13 +80,21 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  if (p.starts_next) launch_dependents();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
+  // Up to here beside the kernel before this one, and from here the next one beside this; a product with v
+  // waits for the kernel before (which makes v, and has itself waited) only where it reads v.
+  if (!LORA) wait_prerequisites();
+  launch_dependents();
   const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
+  // Rows side by side in x: no index, or adapters whose tokens fit one tile, which then takes them in their
+  // own order and looks up where each lies in the sorted one (s_idx; -1: a token that is not named).
+  const bool own_order = LORA && p.R <= NT;
+  const bool box = own_order || p.row_index == nullptr;
+  if (own_order && threadIdx.x < NT) s_idx[threadIdx.x] = -1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -120,29 +129,39 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   // this CTA's share of the contraction: k-blocks of x (k-blocks of adapters follow)
   const int kb0 = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split) : 0;
   const int base = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split) - kb0 : 0;
-  // Few rows of x come by TMA, four a load; from 17 on warps 2..5 copy them.
-  const bool copy = live && valid >= COPY_FROM;
-  const int groups = copy || !live ? 0 : (valid + 3) / 4;
+  // Rows side by side come by TMA in boxes of 32; few others four a load, from 17 on warps 2..5 copy them.
+  const bool copy = live && !box && valid >= COPY_FROM;
+  const int groups = copy || box || !live ? 0 : (valid + 3) / 4;
+  const int boxes = box && live ? (valid + 31) / 32 : 0;
   auto load_w = [&](int step) {
     const uint32_t fb = full0 + 8 * (step % STAGES), dst = smem_u32(s_w + (step % STAGES) * W_STAGE);
     const int k0 = (kb0 + step) * BK;
-    mbar_arrive_expect_tx(fb, W_STAGE + groups * 512u);
+    mbar_arrive_expect_tx(fb, W_STAGE + groups * 512u + boxes * X_BOX);
     if (p.w_km) {
       tma_load_3d(dst, &p.tw, k0, n0, e, fb);
     } else {
       tma_load_3d(dst, &p.tw, n0, k0, e, fb);
       tma_load_3d(dst + W_BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? n0 : n0 + 64, k0, e, fb);
     }
+    for (int b = 0; b < boxes; ++b)
+      tma_load_2d(smem_u32(s_x + (step % STAGES) * X_STAGE) + b * X_BOX, &p.tx_box32, k0, i0 + 32 * b, fb);
   };
   const int ahead = min(base, STAGES);               // W of the first stages is on its way before the rows are known
   if (warp == 0 && lane == 0)
     for (int step = 0; step < ahead; ++step) load_w(step);
   if (live && warp != 0) {
-    // x's row of every row of the tile; -1: the index lies outside x (the row reads as zeros)
-    for (int j = threadIdx.x - 32; j < ((valid + 3) & ~3); j += THREADS - 32) {
-      const int i = i0 + min(j, valid - 1);
-      const int r = p.row_index != nullptr ? __ldg(p.row_index + i) : i;
-      s_idx[j] = r >= 0 && r < p.x_rows ? r : -1;
+    if (own_order) {
+      for (int i = threadIdx.x - 32; i < p.R; i += THREADS - 32) {
+        const int r = __ldg(p.row_index + i);
+        if (r >= 0 && r < p.R) s_idx[r] = i;
+      }
+    } else {
+      // x's row of every row of the tile; -1: the index lies outside x (the row reads as zeros)
+      for (int j = threadIdx.x - 32; j < ((valid + 3) & ~3); j += THREADS - 32) {
+        const int i = i0 + min(j, valid - 1);
+        const int r = p.row_index != nullptr ? __ldg(p.row_index + i) : i;
+        s_idx[j] = r >= 0 && r < p.x_rows ? r : -1;
+      }
     }
     if (LORA && warp == 2) {                         // the adapters that own rows of this tile, ascending
       int n_list = 0;
@@ -171,7 +190,8 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   if (warp == 0 && live) {
     for (int step = 0; step < steps; ++step) {
       const int st = loaded % STAGES;
-      bool ok = mbar_wait_bounded(empty0 + 8 * st, ((loaded / STAGES) & 1) ^ 1, p.budget, abort_flag);
+      // (a stage that was filled ahead may have been used and freed by now: its wait would be for the next round)
+      bool ok = step < ahead || mbar_wait_bounded(empty0 + 8 * st, ((loaded / STAGES) & 1) ^ 1, p.budget, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         if (!*abort_flag) record_timeout(p.status, WAIT_PRODUCER_EMPTY);
@@ -238,7 +258,8 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         const int c0 = 2 * (x0 + step - base);
         for (int ch = 0; ch < min(2, chunks - c0); ++ch) {
           const int a = s_list[(c0 + ch) / per_adapter];
-          const int first = (max(s_off[a], i0) - i0) & ~15, last = (min(s_off[a + 1], i0 + valid) - i0 + 15) & ~15;
+          const int first = own_order ? 0 : (max(s_off[a], i0) - i0) & ~15;
+          const int last = own_order ? n_mma : (min(s_off[a + 1], i0 + valid) - i0 + 15) & ~15;
           const uint32_t id = idesc_bf16_f32(BM, last - first, true, false);
           const uint64_t ad = smem_desc_sw128(w_base + 2048u * ch, W_BOX, 1024u);
           for (int half = 0; half < 2; ++half)
@@ -267,8 +288,9 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
             hi[ch] = lo[ch] = make_uint4(0, 0, 0, 0);
             if (c0 + ch >= chunks) continue;
             const int a = s_list[(c0 + ch) / per_adapter];
-            const int i = i0 + (tid >> 1), k = ((c0 + ch) % per_adapter) * 16 + (tid & 1) * 8;
-            if (i < i0 + valid && i >= s_off[a] && i < s_off[a + 1] && k < p.rank)
+            const int j = tid >> 1, k = ((c0 + ch) % per_adapter) * 16 + (tid & 1) * 8;
+            const int i = j >= valid ? -1 : own_order ? s_idx[j] : i0 + j;
+            if (i >= 0 && i >= s_off[a] && i < s_off[a + 1] && k < p.rank)
               split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k, hi[ch], lo[ch]);
           }
         }
@@ -295,7 +317,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         } else {
           const int row = tid >> 1;
           uint8_t* line = s_x + st * X_STAGE + row * 128;
-          for (int ch = 0; ch < 2; ++ch) {                 // hi in pieces 0..3, lo in 4..7
+          for (int ch = 0; ch < 2 && row < NT; ++ch) {     // hi in pieces 0..3, lo in 4..7
             const int at = 2 * ch + (tid & 1);
             *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) = hi[ch];
             *reinterpret_cast<uint4*>(line + (((at + 4) ^ (row & 7)) << 4)) = lo[ch];
@@ -364,7 +386,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         for (int q = 0; q < 8; ++q) f[q] *= sc;
       }
       if constexpr (LORA) {
-        if (r >= 0) store_row8(p, static_cast<int64_t>(e) * p.R + r, col, f, u);
+        if (r >= 0) store_row8(p, static_cast<int64_t>(e) * p.R + (own_order ? j : r), col, f, u);
       } else {
         store_row8(p, i0 + j, col, f, u);
       }
@@ -413,10 +435,10 @@ tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(p.split);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;    // adapters: starts beside the first product
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;    // starts beside the kernel before
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = LORA ? 2 : 1;
+  cfg.numAttrs = 2;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<SWIGLU, LORA>, p);
   if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_kernel: %s", cudaGetErrorString(err));
   return check_launch("ragged_kernel");
@@ -434,9 +456,10 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the weights");
   if (swiglu && !encode_bf16_3d(&p.tw2, g.w + g.n, g.n, g.K, g.E, 2 * g.n, 64, BK))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the up half of the weights");
-  if (!encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
+  if (g.row_index != nullptr && !encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
-  if (!encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128) || !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, 32))
+  if ((g.row_index == nullptr && !encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128)) ||
+      !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, 32))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
@@ -446,7 +469,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
   p.num_kb = static_cast<int>((g.K + BK - 1) / BK);
   p.L = g.L; p.rank = g.rank;
-  p.act = g.act; p.w_km = g.w_km; p.out_f32 = g.out_f32; p.backward = g.backward; p.starts_next = g.starts_next;
+  p.act = g.act; p.w_km = g.w_km; p.out_f32 = g.out_f32; p.backward = g.backward;
   p.status = status_word();
   p.budget = wait_budget();
   if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");

@@ -39,7 +39,6 @@ struct RaggedParams {
   bool w_km;                  // W stored [E][n][K]
   bool out_f32;
   bool backward;              // multiply by the activation's derivative at h_pre
-  bool starts_next;           // the next kernel may start beside this one
   uint32_t* status;
   unsigned long long budget;
 };
@@ -65,7 +64,6 @@ struct RaggedArgs {
   const float* v;             // adapters, or nullptr
   const uint16_t* lora_b;     // [E][L][rank][n]
   int L, rank;
-  bool starts_next;           // the next launch is a product with v (see RaggedParams)
 };
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
 // The same on CTA pairs (row_tiles: how many tiles of 256 rows there can be).

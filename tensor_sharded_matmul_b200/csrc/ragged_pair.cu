@@ -195,7 +195,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (p.starts_next) launch_dependents();
+  if (!LORA) wait_prerequisites();                   // as in ragged.cu
+  launch_dependents();
   const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
   tc_fence_before();
@@ -579,11 +580,11 @@ tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];                                        // adapters: starts beside the first product
+  cudaLaunchAttribute at[1];                                        // starts beside the kernel before
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = LORA ? 1 : 0;
+  cfg.numAttrs = 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_pair_kernel<SWIGLU, LORA>, p);
   if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_pair_kernel: %s", cudaGetErrorString(err));
   return check_launch("ragged_pair_kernel");

@@ -486,3 +486,61 @@ def test_lora_infinite_values_stay_with_their_token():
     assert not np.isfinite(got[8]).any()
     slack = size * ((2 * k + 2 * rank) * 2.0 ** -23 + 2.0 ** -16)
     within(got[keep], ref[0][keep], (slack + 2.0 ** -8 * (np.abs(ref[0]) + slack))[keep], "other tokens")
+
+
+@pytest.mark.parametrize("N", [1, 40, 64, 100])
+def test_lora_calls_back_to_back(N):
+    """Many calls on one stream with nothing between them (each kernel begins beside the one before it), over several
+    sets of buffers: every result is the one of a call by itself, bit for bit, and no wait runs out."""
+    k, n, t, L, rank = 2048, 1024, 2, 4, 16
+    sets = []
+    for seed in range(3):
+        d = S.Draw(seed, "cuda")
+        ids = torch.randint(-1, L, (N,), generator=d.gen, device="cuda", dtype=torch.int32)
+        off, tok, _ = M.sort_rows(ids.cpu().numpy()[:, None], L, rest=True)
+        sets.append(dict(x=d.normal((N, k)), w=d.normal((t, k, n // t), 0.02), a=d.normal((L, k, rank), 0.02),
+                         b=d.normal((t, L, rank, n // t), 0.5), off=dev(off), tok=dev(tok),
+                         ws=torch.empty(N * rank, device="cuda"), y=torch.zeros((t, N, n // t), dtype=torch.bfloat16, device="cuda")))
+
+    def call(s):
+        tp.tp_lora_linear(s["x"], N, k, n, t, s["w"], L, rank, s["a"], s["b"], None, s["off"], s["tok"], s["y"], s["ws"], N * rank * 4)
+
+    want = []
+    for s in sets:
+        call(s)
+        settled()
+        want.append(s["y"].clone())
+        s["y"].zero_()
+    for i in range(90):
+        call(sets[i % 3])
+    settled()
+    for s, w in zip(sets, want):
+        assert torch.equal(s["y"], w)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 64, 300])
+def test_products_back_to_back(rows):
+    """The same of the expert products: up (gathered), down, gradient, a chain of calls that read each other's
+    outputs."""
+    E, k, n = 4, 1024, 512
+    d = S.Draw(rows, "cuda")
+    off, idx, R = plan_of([rows] * E, 64, rows)
+    off, idx = dev(off), dev(idx)
+    x, w1, w2 = d.normal((64, k)), d.normal((E, k, 2 * n), 0.03), d.normal((E, n, k), 0.03)
+    z, u = (torch.zeros((R, m), dtype=torch.bfloat16, device="cuda") for m in (n, k))
+    pre, dh = (torch.zeros((R, 2 * n), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def chain(check=lambda: None):
+        tp.tp_ragged_linear(x, 64, idx, off, R, E, k, n, tp.TP_ACT_SWIGLU, w1, z, tp.TP_BF16, pre)
+        check()
+        tp.tp_ragged_linear(z, R, None, off, R, E, n, k, tp.TP_ACT_NONE, w2, u, tp.TP_BF16)
+        check()
+        tp.tp_ragged_linear_dx(u, off, R, E, n, k, w2, tp.TP_ACT_SWIGLU, pre, dh)
+        check()
+
+    chain(settled)
+    want = [v.clone() for v in (z, u, dh)]
+    for _ in range(40):
+        chain()
+    settled()
+    assert all(torch.equal(a, b) for a, b in zip((z, u, dh), want))
