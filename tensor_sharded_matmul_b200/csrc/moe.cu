@@ -25,6 +25,12 @@ constexpr int WORDS = TB / 32;
 template <int VPL>
 constexpr int ROUTE_THREADS = VPL <= 8 ? 1024 : 512;      // registers of a long list
 
+// See launch_beside.
+__device__ __forceinline__ void begin_beside() {
+  wait_prerequisites();
+  launch_dependents();
+}
+
 // Order-preserving integer of a float (no NaN): a < b <=> key(a) < key(b). key(-inf) = 0x007fffff.
 constexpr uint32_t KEY_MASKED = 0x007fffffu;
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -37,7 +43,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* logits, int64_t at) {
-  const float x = BF16 ? bf(__ldg(static_cast<const uint16_t*>(logits) + at)) : __ldg(static_cast<const float*>(logits) + at);
+  const float x = BF16 ? bf(ld_u16(static_cast<const uint16_t*>(logits) + at)) : ld_f32(static_cast<const float*>(logits) + at);
   // NaN masks like -inf; +inf counts as the largest finite number
   return x != x ? -INFINITY : fminf(x, FLT_MAX);
 }
@@ -152,8 +158,8 @@ __device__ __forceinline__ void sort_lane(uint32_t (&key)[VPL], int (&at)[VPL]) 
 }
 
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(ROUTE_THREADS<VPL>) route_kernel(const void* __restrict__ logits, int gate,
-                                                              float* __restrict__ weight, SortParams p) {
+__global__ void __launch_bounds__(ROUTE_THREADS<VPL>) route_kernel(const void* logits, int gate,
+                                                              float* weight, SortParams p) {
   extern __shared__ int s_dyn[];
   uint32_t* bits = reinterpret_cast<uint32_t*>(s_dyn);         // [E][WORDS]
   int* start = s_dyn + p.E * WORDS;                            // [E + 1]
@@ -162,8 +168,9 @@ __global__ void __launch_bounds__(ROUTE_THREADS<VPL>) route_kernel(const void* _
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
   clear_bits(bits, p.E);
+  begin_beside();
   __syncthreads();
-  for (int t = warp; t < TB && n0 + t < p.N; t += ROUTE_THREADS<VPL> / 32) {
+  for (int t = warp; t < TB && n0 + t < p.N; t += blockDim.x / 32) {
     const int64_t n = n0 + t;
     uint32_t key[VPL];
     int at[VPL];                                               // the expert of each key
@@ -238,6 +245,7 @@ __global__ void __launch_bounds__(256) sort_count_kernel(SortParams p) {
   int* s_pick = start + buckets + 1;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
   clear_bits(bits, buckets);
+  begin_beside();
   __syncthreads();
   for (int i = threadIdx.x; i < TB * p.k && n0 + i / p.k < p.N; i += blockDim.x) {
     int e = p.expert[n0 * p.k + i];
@@ -254,6 +262,7 @@ __global__ void __launch_bounds__(256) sort_scan_kernel(SortParams p) {
   const int lane = threadIdx.x % 32;
   const int e = blockIdx.x * 8 + threadIdx.x / 32;
   const int buckets = p.E + p.rest;
+  begin_beside();
   if (e >= buckets) return;
   int32_t* c = p.counts + static_cast<int64_t>(e) * p.blocks;
   int base = 0;
@@ -276,6 +285,7 @@ __global__ void __launch_bounds__(256) sort_place_kernel(SortParams p) {
   extern __shared__ int start[];
   const int buckets = p.E + p.rest;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
+  begin_beside();
   for (int e = threadIdx.x; e < buckets; e += blockDim.x)
     start[e] = p.counts[static_cast<int64_t>(buckets) * p.blocks + e];
   __syncthreads();
@@ -300,11 +310,12 @@ __global__ void __launch_bounds__(256) sort_place_kernel(SortParams p) {
 // (TOPK: zero) for its experts; then lane j writes the j-th choice's, from its own copy of that logit. A
 // choice that is named twice has the sum of its dw.
 template <int VPL, bool BF16>
-__global__ void __launch_bounds__(256) route_bwd_kernel(const void* __restrict__ logits, int64_t N, int E, int k, int gate,
-                                                        const int32_t* __restrict__ expert,
-                                                        const float* __restrict__ dweight, void* dlogits) {
+__global__ void __launch_bounds__(256) route_bwd_kernel(const void* logits, int64_t N, int E, int k, int gate,
+                                                        const int32_t* expert,
+                                                        const float* dweight, void* dlogits) {
   const int lane = threadIdx.x % 32;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  begin_beside();
   if (n >= N) return;
   float v[VPL];
   if (gate == TP_GATE_SOFTMAX) {
@@ -314,9 +325,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const void* __restrict__
       v[i] = e < E ? load_logit<BF16>(logits, n * E + e) : -INFINITY;
     }
   }
-  int my_e = lane < k ? __ldg(expert + n * k + lane) : -1;
+  int my_e = lane < k ? ld_s32(expert + n * k + lane) : -1;
   if (my_e >= E) my_e = -1;
-  float my_d = my_e >= 0 ? __ldg(dweight + n * k + lane) : 0.0f;
+  float my_d = my_e >= 0 ? ld_f32(dweight + n * k + lane) : 0.0f;
   const float my_v = my_e >= 0 ? load_logit<BF16>(logits, n * E + my_e) : -INFINITY;
   bool first = my_e >= 0, again = false;           // the lowest lane of equal choices takes the sum of their dw
   for (int j = 0; j < k; ++j) {
@@ -384,10 +395,10 @@ struct Raw8 {
   uint4 a, b;
   __device__ __forceinline__ void load(const void* base, int64_t at) {
     if constexpr (BF16) {
-      a = ld_nc_v4(static_cast<const uint16_t*>(base) + at);
+      a = ld_stream_v4(static_cast<const uint16_t*>(base) + at);
     } else {
-      a = ld_nc_v4(static_cast<const float*>(base) + at);
-      b = ld_nc_v4(static_cast<const float*>(base) + at + 4);
+      a = ld_stream_v4(static_cast<const float*>(base) + at);
+      b = ld_stream_v4(static_cast<const float*>(base) + at + 4);
     }
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
@@ -402,11 +413,12 @@ struct Raw8 {
 };
 
 template <int KMAX, bool U_BF16, bool Y_BF16>
-__global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u, int64_t R, const float* __restrict__ weight,
-                                                      const int32_t* __restrict__ slot, int64_t N, int h, int k,
-                                                      void* __restrict__ y) {
+__global__ void __launch_bounds__(256) combine_kernel(const void* u, int64_t R, const float* weight,
+                                                      const int32_t* slot, int64_t N, int h, int k,
+                                                      void* y) {
   const int per_row = h / 8;
   const int64_t items = N * per_row;
+  begin_beside();
   for (int64_t it = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; it < items;
        it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t n = it / per_row;
@@ -419,9 +431,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u
       float w[KMAX];
 #pragma unroll
       for (int j = 0; j < KMAX; ++j) {
-        const int s = j0 + j < k ? __ldg(slot + n * k + j0 + j) : -1;
+        const int s = j0 + j < k ? ld_s32(slot + n * k + j0 + j) : -1;
         const bool in = s >= 0 && s < R;
-        w[j] = !in ? 0.0f : weight != nullptr ? __ldg(weight + n * k + j0 + j) : 1.0f;
+        w[j] = !in ? 0.0f : weight != nullptr ? ld_f32(weight + n * k + j0 + j) : 1.0f;
         raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
         if (in) raw[j].load(u, static_cast<int64_t>(s) * h + col);
       }
@@ -444,20 +456,21 @@ __global__ void __launch_bounds__(256) combine_kernel(const void* __restrict__ u
 }
 
 template <int KMAX, bool DY_BF16, bool U_BF16>
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ u, int64_t R,
-                                                          const float* __restrict__ weight, const int32_t* __restrict__ slot,
-                                                          int64_t N, int h, int k, uint16_t* __restrict__ du,
-                                                          float* __restrict__ dweight) {
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const void* dy, const void* u, int64_t R,
+                                                          const float* weight, const int32_t* slot,
+                                                          int64_t N, int h, int k, uint16_t* du,
+                                                          float* dweight) {
   const int lane = threadIdx.x % 32;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+  begin_beside();
   if (n >= N) return;
   int s[KMAX];
   float w[KMAX], dot[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
-    s[j] = j < k ? __ldg(slot + n * k + j) : -1;
+    s[j] = j < k ? ld_s32(slot + n * k + j) : -1;
     if (s[j] >= R) s[j] = -1;
-    w[j] = s[j] >= 0 ? __ldg(weight + n * k + j) : 0.0f;
+    w[j] = s[j] >= 0 ? ld_f32(weight + n * k + j) : 0.0f;
     dot[j] = 0.0f;
   }
   for (int col = lane * 8; col < h; col += 256) {
@@ -494,11 +507,12 @@ template <bool BF16>
 tp_status launch_route(const void* logits, int gate, float* weight, const SortParams& p, cudaStream_t s) {
   const size_t smem = (static_cast<size_t>(p.E) * WORDS + p.E + 1 + TB * p.k) * 4;
   const int vpl = (p.E + 31) / 32;
-  if (vpl <= 2) route_kernel<2, BF16><<<p.blocks, ROUTE_THREADS<2>, smem, s>>>(logits, gate, weight, p);
-  else if (vpl <= 4) route_kernel<4, BF16><<<p.blocks, ROUTE_THREADS<4>, smem, s>>>(logits, gate, weight, p);
-  else if (vpl <= 8) route_kernel<8, BF16><<<p.blocks, ROUTE_THREADS<8>, smem, s>>>(logits, gate, weight, p);
-  else route_kernel<32, BF16><<<p.blocks, ROUTE_THREADS<32>, smem, s>>>(logits, gate, weight, p);
-  return check_launch("route_kernel");
+  // a warp for each token, and four at least to place them
+  auto threads = [&](int most) { return p.N >= most / 32 ? most : p.N > 4 ? 32 * static_cast<int>(p.N) : 128; };
+  if (vpl <= 2) return launch_beside("route_kernel", route_kernel<2, BF16>, p.blocks, threads(ROUTE_THREADS<2>), smem, s, logits, gate, weight, p);
+  if (vpl <= 4) return launch_beside("route_kernel", route_kernel<4, BF16>, p.blocks, threads(ROUTE_THREADS<4>), smem, s, logits, gate, weight, p);
+  if (vpl <= 8) return launch_beside("route_kernel", route_kernel<8, BF16>, p.blocks, threads(ROUTE_THREADS<8>), smem, s, logits, gate, weight, p);
+  return launch_beside("route_kernel", route_kernel<32, BF16>, p.blocks, threads(ROUTE_THREADS<32>), smem, s, logits, gate, weight, p);
 }
 
 template <bool BF16>
@@ -506,20 +520,17 @@ tp_status launch_route_bwd(const void* logits, int64_t N, int E, int k, int gate
                            const float* dweight, void* dlogits, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((N + 7) / 8);
   const int vpl = (E + 31) / 32;
-  if (vpl <= 2) route_bwd_kernel<2, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
-  else if (vpl <= 4) route_bwd_kernel<4, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
-  else if (vpl <= 8) route_bwd_kernel<8, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
-  else route_bwd_kernel<32, BF16><<<grid, 256, 0, s>>>(logits, N, E, k, gate, expert, dweight, dlogits);
-  return check_launch("route_bwd_kernel");
+  if (vpl <= 2) return launch_beside("route_bwd_kernel", route_bwd_kernel<2, BF16>, grid, 256, 0, s, logits, N, E, k, gate, expert, dweight, dlogits);
+  if (vpl <= 4) return launch_beside("route_bwd_kernel", route_bwd_kernel<4, BF16>, grid, 256, 0, s, logits, N, E, k, gate, expert, dweight, dlogits);
+  if (vpl <= 8) return launch_beside("route_bwd_kernel", route_bwd_kernel<8, BF16>, grid, 256, 0, s, logits, N, E, k, gate, expert, dweight, dlogits);
+  return launch_beside("route_bwd_kernel", route_bwd_kernel<32, BF16>, grid, 256, 0, s, logits, N, E, k, gate, expert, dweight, dlogits);
 }
 
 // Offsets and places of a batch of more than one block, from the counts of its blocks.
 tp_status scan_and_place(const SortParams& p, cudaStream_t s) {
   const int buckets = p.E + p.rest;
-  sort_scan_kernel<<<(buckets + 7) / 8, 256, 0, s>>>(p);
-  if (tp_status st = check_launch("sort_scan_kernel")) return st;
-  sort_place_kernel<<<p.blocks, 256, static_cast<size_t>(buckets + 1) * 4, s>>>(p);
-  return check_launch("sort_place_kernel");
+  if (tp_status st = launch_beside("sort_scan_kernel", sort_scan_kernel, (buckets + 7) / 8, 256, 0, s, p)) return st;
+  return launch_beside("sort_place_kernel", sort_place_kernel, p.blocks, 256, static_cast<size_t>(buckets + 1) * 4, s, p);
 }
 
 int64_t sort_blocks(int64_t N) { return (N + TB - 1) / TB; }
@@ -535,9 +546,8 @@ tp_status launch_combine(const void* u, int64_t R, const float* weight, const in
   const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
   if (cap <= 0) return fail(TP_ECUDA, "cannot query the SM count");
   const unsigned grid = static_cast<unsigned>(blocks < cap ? blocks : cap);
-  if (y_bf16) combine_kernel<KMAX, U_BF16, true><<<grid, 256, 0, s>>>(u, R, weight, slot, N, h, k, y);
-  else combine_kernel<KMAX, U_BF16, false><<<grid, 256, 0, s>>>(u, R, weight, slot, N, h, k, y);
-  return check_launch("combine_kernel");
+  if (y_bf16) return launch_beside("combine_kernel", combine_kernel<KMAX, U_BF16, true>, grid, 256, 0, s, u, R, weight, slot, N, h, k, y);
+  return launch_beside("combine_kernel", combine_kernel<KMAX, U_BF16, false>, grid, 256, 0, s, u, R, weight, slot, N, h, k, y);
 }
 
 template <int KMAX>
@@ -545,14 +555,12 @@ tp_status launch_combine_bwd(const void* dy, bool dy_bf16, const void* u, bool u
                              const int32_t* slot, int64_t N, int h, int k, uint16_t* du, float* dweight, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((N + 7) / 8);
   if (dy_bf16 && u_bf16)
-    combine_bwd_kernel<KMAX, true, true><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
-  else if (dy_bf16)
-    combine_bwd_kernel<KMAX, true, false><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
-  else if (u_bf16)
-    combine_bwd_kernel<KMAX, false, true><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
-  else
-    combine_bwd_kernel<KMAX, false, false><<<grid, 256, 0, s>>>(dy, u, R, weight, slot, N, h, k, du, dweight);
-  return check_launch("combine_bwd_kernel");
+    return launch_beside("combine_bwd_kernel", combine_bwd_kernel<KMAX, true, true>, grid, 256, 0, s, dy, u, R, weight, slot, N, h, k, du, dweight);
+  if (dy_bf16)
+    return launch_beside("combine_bwd_kernel", combine_bwd_kernel<KMAX, true, false>, grid, 256, 0, s, dy, u, R, weight, slot, N, h, k, du, dweight);
+  if (u_bf16)
+    return launch_beside("combine_bwd_kernel", combine_bwd_kernel<KMAX, false, true>, grid, 256, 0, s, dy, u, R, weight, slot, N, h, k, du, dweight);
+  return launch_beside("combine_bwd_kernel", combine_bwd_kernel<KMAX, false, false>, grid, 256, 0, s, dy, u, R, weight, slot, N, h, k, du, dweight);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -795,8 +803,9 @@ tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, in
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return fail(TP_ENOSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
   SortParams p = {N, L, 1, 1, static_cast<int>(sort_blocks(N)), const_cast<int32_t*>(id), nullptr, offsets, row_token,
                   static_cast<int32_t*>(ws), static_cast<int32_t*>(ws) + (L + 1) * (sort_blocks(N) + 1)};
-  sort_count_kernel<<<p.blocks, 256, (static_cast<size_t>(L + 1) * WORDS + L + 2 + TB) * 4, s>>>(p);
-  if (tp_status st = check_launch("sort_count_kernel")) return st;
+  if (tp_status st = launch_beside("sort_count_kernel", sort_count_kernel, p.blocks, 256,
+                                   (static_cast<size_t>(L + 1) * WORDS + L + 2 + TB) * 4, s, p))
+    return st;
   return p.blocks == 1 ? TP_OK : scan_and_place(p, s);
 }
 

@@ -152,14 +152,14 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   if (live && warp != 0) {
     if (own_order) {
       for (int i = threadIdx.x - 32; i < p.R; i += THREADS - 32) {
-        const int r = __ldg(p.row_index + i);
+        const int r = ld_s32(p.row_index + i);
         if (r >= 0 && r < p.R) s_idx[r] = i;
       }
     } else {
       // x's row of every row of the tile; -1: the index lies outside x (the row reads as zeros)
       for (int j = threadIdx.x - 32; j < ((valid + 3) & ~3); j += THREADS - 32) {
         const int i = i0 + min(j, valid - 1);
-        const int r = p.row_index != nullptr ? __ldg(p.row_index + i) : i;
+        const int r = p.row_index != nullptr ? ld_s32(p.row_index + i) : i;
         s_idx[j] = r >= 0 && r < p.x_rows ? r : -1;
       }
     }
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         for (int q = 0; q < 8; ++q) f[q] = u[q] = 0.0f;
       }
       if (p.seg_scale != nullptr) {
-        const float sc = __ldg(p.seg_scale + e);
+        const float sc = ld_f32(p.seg_scale + e);
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[q] *= sc;
       }

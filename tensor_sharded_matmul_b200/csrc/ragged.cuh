@@ -9,6 +9,8 @@
 
 #include <cuda.h>
 
+#include <utility>
+
 #include "act.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
@@ -42,6 +44,26 @@ struct RaggedParams {
   uint32_t* status;
   unsigned long long budget;
 };
+
+// Launches a kernel that may begin while the one before it on the stream still runs: it waits
+// (wait_prerequisites) before it touches global memory, and then lets the next one begin. Back to back
+// such launches hide about 2 us each: the launch and, for the products, barriers and TMEM.
+template <typename... P, typename... A>
+tp_status launch_beside(const char* what, void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  if (err != cudaSuccess) return fail(TP_ECUDA, "%s: %s", what, cudaGetErrorString(err));
+  return check_launch(what);
+}
 
 // Host-side arguments of ragged_product (checked by the entry points).
 struct RaggedArgs {
@@ -86,7 +108,7 @@ tp_status ragged_dw(const RaggedDwArgs& g, cudaStream_t s);
 
 // offsets[e], clamped to the rows that exist.
 __device__ __forceinline__ int seg_bound(const int32_t* offsets, int e, int R) {
-  return min(max(__ldg(offsets + e), 0), R);
+  return min(max(ld_s32(offsets + e), 0), R);
 }
 
 // Tile number g among all segments' row tiles of NT rows (segment ascending): its segment, and the
@@ -162,10 +184,10 @@ __device__ __forceinline__ float apply_act(float x, int act) {
 // gradient there.
 __device__ __forceinline__ void load_h_pre(const RaggedParams& p, int64_t row, int col, uint4& h0, uint4& h1) {
   if (p.act == TP_ACT_SWIGLU) {
-    h0 = ld_nc_v4(p.h_pre + row * 2 * p.n + col);
-    h1 = ld_nc_v4(p.h_pre + row * 2 * p.n + p.n + col);
+    h0 = ld_stream_v4(p.h_pre + row * 2 * p.n + col);
+    h1 = ld_stream_v4(p.h_pre + row * 2 * p.n + p.n + col);
   } else if (p.act != TP_ACT_NONE) {
-    h0 = ld_nc_v4(p.h_pre + row * p.n + col);
+    h0 = ld_stream_v4(p.h_pre + row * p.n + col);
   }
 }
 __device__ __forceinline__ void store_backward8(const RaggedParams& p, int64_t row, int col, float (&f)[8], uint4 h0, uint4 h1) {

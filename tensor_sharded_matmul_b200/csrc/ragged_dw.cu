@@ -134,6 +134,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
+  wait_prerequisites();
+  launch_dependents();
   c.full0_leader = mapa_shared(c.full0, 0);
   c.acce0_leader = mapa_shared(c.acce0, 0);
   const uint32_t tmem_base = *tmem_slot;
@@ -271,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
 #pragma unroll
           for (int i = 0; i < BK / STEP; ++i) {
             const int at = r + h * BK + row0 + STEP * i;
-            idx[h][i] = at < end ? __ldg(p.row_index + at) : -1;
+            idx[h][i] = at < end ? ld_s32(p.row_index + at) : -1;
           }
         ok = mbar_wait_bounded(c.empty0 + 8 * st, phase ^ 1u, p.budget, c.abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -423,8 +425,7 @@ tp_status launch_dw(const DwParams& p, cudaStream_t s) {
   const int sms = sm_count();
   int grid = 2 * static_cast<int64_t>(p.units) < sms ? 2 * p.units : (sms & ~1);
   if (grid < 2) grid = 2;
-  ragged_dw_kernel<GATHER><<<grid, THREADS<GATHER>, SMEM, s>>>(p);
-  return check_launch("ragged_dw_kernel");
+  return launch_beside("ragged_dw_kernel", ragged_dw_kernel<GATHER>, grid, THREADS<GATHER>, SMEM, s, p);
 }
 
 }  // namespace

@@ -123,7 +123,7 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
 __device__ __forceinline__ uint32_t runs_of_half(const RaggedParams& p, int first, int mine, int lane, int (&begin)[4]) {
   int r[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) r[g] = 32 * g + lane < mine ? __ldg(p.row_index + first + 32 * g + lane) : 0;
+  for (int g = 0; g < 4; ++g) r[g] = 32 * g + lane < mine ? ld_s32(p.row_index + first + 32 * g + lane) : 0;
   uint32_t runs = 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -407,12 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             continue;
           }
           if (!LORA && p.seg_scale != nullptr) {
-            const float sc = __ldg(p.seg_scale + t.e);
+            const float sc = ld_f32(p.seg_scale + t.e);
 #pragma unroll
             for (int q = 0; q < 8; ++q) f[q] *= sc;
           }
           if constexpr (LORA) {
-            const int r = __ldg(p.row_index + i);
+            const int r = ld_s32(p.row_index + i);
             if (r >= 0 && r < p.x_rows) store_row8(p, static_cast<int64_t>(t.e) * p.R + r, col, f, up);
           } else {
             store_row8(p, i, col, f, up);
@@ -449,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int row = r0 + STEP * i;
         idx[i] = -2;                                   // no row: left as it is (its column is not read)
         if (row < mine && !(runs >> (row >> 5) & 1)) {
-          const int r = __ldg(p.row_index + t.i0 + half0 + row);
+          const int r = ld_s32(p.row_index + t.i0 + half0 + row);
           idx[i] = r >= 0 && r < p.x_rows ? r : -1;    // -1: outside x, zeros
         }
       }
@@ -575,19 +575,7 @@ tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
   const int sms = sm_count();
   int grid = 2 * units < sms ? static_cast<int>(2 * units) : (sms & ~1);
   if (grid < 2) grid = 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];                                        // starts beside the kernel before
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_pair_kernel<SWIGLU, LORA>, p);
-  if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_pair_kernel: %s", cudaGetErrorString(err));
-  return check_launch("ragged_pair_kernel");
+  return launch_beside("ragged_pair_kernel", ragged_pair_kernel<SWIGLU, LORA>, grid, THREADS, SMEM, s, p);
 }
 
 }  // namespace
