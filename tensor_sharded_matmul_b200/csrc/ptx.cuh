@@ -322,21 +322,21 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
                : "l"(p));
   return v;
 }
-// Loads for kernels that begin beside the one before them (wait_prerequisites): coherent, and not moved
-// before the wait, as loads marked read-only may be.
+// Loads for kernels that begin beside the one before them (wait_prerequisites): coherent, and (volatile) not
+// moved before the wait, as loads marked read-only may be.
 __device__ __forceinline__ int ld_s32(const int32_t* p) {
   int v;
-  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ float ld_f32(const float* p) {
   float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint16_t ld_u16(const uint16_t* p) {
   uint16_t v;
-  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
@@ -344,7 +344,7 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p)
-               : "memory");
+              );
   return v;
 }
 // L2-only load (skips L1): for data this kernel wrote earlier and now reads back.
