@@ -38,16 +38,25 @@ constexpr int COPY_FROM = 17;                 // rows of a tile from which cp.as
 constexpr int STG_LD = BM + 4;                // floats between rows of the staged output tile
 constexpr int MAX_SEGS = TP_MAX_EXPERTS;
 
-constexpr int NT = 64;                        // rows per tile, at most
-constexpr uint32_t X_STAGE = NT * BK * 2;     // 8 KiB
-constexpr uint32_t X_BOX = 32 * BK * 2;       // 32 rows
-constexpr uint32_t TMEM_COLS = NT;
-static_assert(TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM is allocated in powers of two from 32 columns");
-static_assert(STAGES % 2 == 0, "the indices behind the 3 * STAGES + 4 barriers start on 16 bytes");
-constexpr size_t SMEM = 1024 + STAGES * (W_STAGE + X_STAGE) + (3 * STAGES + 4) * 8 + 16 + (MAX_SEGS + 4) * 4 + 2 * NT * 4;
+constexpr size_t TWO_PER_SM = 80 * 1024;      // more than a third of an SM's shared memory
+// A tile has 64 rows at most, or 16: then a CTA's stages take 72 KiB instead of 96, and three of them fit an SM.
+template <int NT>
+constexpr uint32_t X_STAGE = NT * BK * 2;
+template <int NT>
+constexpr int BOX_ROWS = NT < 32 ? NT : 32;   // rows of x that one load brings when they lie side by side
+// Dynamic shared memory: stages, barriers, the segments' bounds, the tile's rows and adapters.
+template <int NT>
+size_t smem_bytes(int segs) {
+  return 1024 + STAGES * (W_STAGE + X_STAGE<NT>) + (3 * STAGES + 4) * 8 + 16 + ((segs + 4) & ~3) * 4 + 2 * NT * 4;
+}
 
-template <bool SWIGLU, bool LORA>
+template <int NT, bool SWIGLU, bool LORA>
 __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__ RaggedParams p) {
+  constexpr uint32_t X_STAGE = tpx::X_STAGE<NT>;
+  constexpr uint32_t X_BOX = BOX_ROWS<NT> * BK * 2;
+  constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  static_assert(NT % 16 == 0 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM is allocated in powers of two from 32 columns");
+  static_assert(STAGES % 2 == 0, "the bounds behind the 3 * STAGES + 4 barriers start on 16 bytes");
   static_assert(NT * STG_LD * 4 <= STAGES * (W_STAGE + NT * BK * 2), "the staged output tile reuses the operand stages");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -60,7 +69,8 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int* s_count = reinterpret_cast<int*>(tmem_slot + 2);            // adapters of this tile
   int* s_off = reinterpret_cast<int*>(bars + 3 * STAGES + 4) + 4;  // 16-byte aligned
-  int* s_idx = s_off + MAX_SEGS + 4;
+  const int segs = LORA ? p.L : p.E;
+  int* s_idx = s_off + ((segs + 4) & ~3);
   int* s_list = s_idx + NT;
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -88,7 +98,6 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   // waits for the kernel before (which makes v, and has itself waited) only where it reads v.
   if (!LORA) wait_prerequisites();
   launch_dependents();
-  const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
   // Rows side by side in x: no index, or adapters whose tokens fit one tile, which then takes them in their
   // own order and looks up where each lies in the sorted one (s_idx; -1: a token that is not named).
@@ -129,10 +138,10 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   // this CTA's share of the contraction: k-blocks of x (k-blocks of adapters follow)
   const int kb0 = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split) : 0;
   const int base = live ? static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split) - kb0 : 0;
-  // Rows side by side come by TMA in boxes of 32; few others four a load, from 17 on warps 2..5 copy them.
+  // Rows side by side come by TMA in boxes of 32 (16); few others four a load, from 17 on warps 2..5 copy them.
   const bool copy = live && !box && valid >= COPY_FROM;
   const int groups = copy || box || !live ? 0 : (valid + 3) / 4;
-  const int boxes = box && live ? (valid + 31) / 32 : 0;
+  const int boxes = box && live ? (valid + BOX_ROWS<NT> - 1) / BOX_ROWS<NT> : 0;
   auto load_w = [&](int step) {
     const uint32_t fb = full0 + 8 * (step % STAGES), dst = smem_u32(s_w + (step % STAGES) * W_STAGE);
     const int k0 = (kb0 + step) * BK;
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
       tma_load_3d(dst + W_BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? n0 : n0 + 64, k0, e, fb);
     }
     for (int b = 0; b < boxes; ++b)
-      tma_load_2d(smem_u32(s_x + (step % STAGES) * X_STAGE) + b * X_BOX, &p.tx_box32, k0, i0 + 32 * b, fb);
+      tma_load_2d(smem_u32(s_x + (step % STAGES) * X_STAGE) + b * X_BOX, &p.tx_box32, k0, i0 + BOX_ROWS<NT> * b, fb);
   };
   const int ahead = min(base, STAGES);               // W of the first stages is on its way before the rows are known
   if (warp == 0 && lane == 0)
@@ -414,22 +423,28 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <bool SWIGLU, bool LORA>
+template <int NT, bool SWIGLU, bool LORA>
 tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
   static int configured_for[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return fail(TP_ECUDA, "cudaGetDevice failed");
   if (dev < 0 || dev >= 64 || !configured_for[dev]) {
-    if (cudaFuncSetAttribute(ragged_kernel<SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(SMEM)) != cudaSuccess)
-      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", SMEM);
+    if (cudaFuncSetAttribute(ragged_kernel<NT, SWIGLU, LORA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem_bytes<NT>(MAX_SEGS) > TWO_PER_SM ? smem_bytes<NT>(MAX_SEGS) : TWO_PER_SM)) != cudaSuccess)
+      return fail(TP_ECUDA, "cannot reserve %zu bytes of shared memory", smem_bytes<NT>(MAX_SEGS));
     if (dev >= 0 && dev < 64) configured_for[dev] = 1;
   }
   if (units * p.split > INT32_MAX) return fail(TP_ESHAPE, "too many tiles");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * p.split));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  // Low tiles: three CTAs on an SM, but two (by asking for more shared memory) where the grid is neither
+  // well below one round of three nor several: 1104 CTAs 86 us by threes, 96 by twos; 448 CTAs 91 and 80
+  // (444 fit at once), 256 CTAs 163 and 130 (some SMs get three, others one).
+  size_t smem = smem_bytes<NT>(LORA ? p.L : p.E);
+  const int64_t ctas = units * p.split, sms = sm_count();
+  if (NT < 64 && 2 * ctas > 3 * sms && ctas < 6 * sms && smem < TWO_PER_SM) smem = TWO_PER_SM;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -439,7 +454,7 @@ tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<SWIGLU, LORA>, p);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, ragged_kernel<NT, SWIGLU, LORA>, p);
   if (err != cudaSuccess) return fail(TP_ECUDA, "ragged_kernel: %s", cudaGetErrorString(err));
   return check_launch("ragged_kernel");
 }
@@ -451,6 +466,16 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   std::memset(&p, 0, sizeof(p));
   const bool lora = g.v != nullptr;
   const bool swiglu = g.act == TP_ACT_SWIGLU && !g.backward;
+  const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
+  // Pairs for segments of more than 64 rows on average, if their tiles (256 rows x 256 columns) keep at
+  // least half of the pairs busy. x A of 4000 tokens, 8 adapters of rank 64, K = 4096: 23 tiles of pairs,
+  // 52 us; 284 CTAs here, 14 us.
+  const int64_t wide_rows = lora ? (g.R + 255) / 256 : g.R / 256 + segs;
+  const int64_t wide_units = wide_rows * ((g.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256)) * (lora ? g.E : 1);
+  const bool pairs = g.R > 64 * segs && 4 * wide_units >= sm_count();
+  // Low tiles where segments have eight rows or fewer on average (most then fit one).
+  const bool low = !pairs && g.R <= 8 * segs;
+  const int nt = low ? 16 : 64;
   if (g.w_km ? !encode_bf16_3d(&p.tw, g.w, g.K, g.n, g.E, g.K, BK, BM)
              : !encode_bf16_3d(&p.tw, g.w, g.n, g.K, g.E, swiglu ? 2 * g.n : g.n, 64, BK))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the weights");
@@ -459,7 +484,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   if (g.row_index != nullptr && !encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if ((g.row_index == nullptr && !encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128)) ||
-      !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, 32))
+      !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, low ? BOX_ROWS<16> : BOX_ROWS<64>))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
@@ -475,22 +500,20 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   if (p.status == nullptr) return fail(TP_ECUDA, "cannot resolve the device status word");
   const int tile_n = swiglu ? BM / 2 : BM;
   p.tiles_n = static_cast<int>((g.n + tile_n - 1) / tile_n);
-  const int64_t segs = lora ? 1 : (g.E < g.R ? g.E : g.R);       // segments that can hold rows
-  // Pairs for segments of more than 64 rows on average, if their tiles (256 rows x 256 columns) keep at
-  // least half of the pairs busy. x A of 4000 tokens, 8 adapters of rank 64, K = 4096: 23 tiles of pairs,
-  // 52 us; 284 CTAs here, 14 us.
-  const int64_t wide_rows = lora ? (g.R + 255) / 256 : g.R / 256 + segs;
-  const int64_t wide_units = wide_rows * ((g.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256)) * (lora ? g.E : 1);
-  if (g.R > 64 * segs && 4 * wide_units >= sm_count()) return ragged_pairs(p, swiglu, lora, wide_rows, s);
-  const int64_t units = (lora ? (g.R + NT - 1) / NT : g.R / NT + segs) * p.tiles_n * (lora ? g.E : 1);
-  // Two CTAs fit an SM: split the contraction (in shares of four k-blocks at least) by powers of two while
-  // all CTAs find room at once. 50 MB of W for one token: 35 us unsplit, 23 by two, 20 by four, 27 by
-  // eight (more than fit), 29 by six (clusters of six pack badly).
+  if (pairs) return ragged_pairs(p, swiglu, lora, wide_rows, s);
+  const int64_t units = (lora ? (g.R + nt - 1) / nt : g.R / nt + segs) * p.tiles_n * (lora ? g.E : 1);
+  // Two CTAs fit an SM (three of low tiles): split the contraction (in shares of four k-blocks at least) by
+  // powers of two while all CTAs find room at once. 50 MB of W for one token: 35 us unsplit, 23 by two, 20
+  // by four, 27 by eight (more than fit), 29 by six (clusters of six pack badly).
   const int64_t room = 2ll * sm_count();
   p.split = 1;
   while (p.split < 8 && units * p.split * 2 <= room && p.num_kb >= 8 * p.split) p.split *= 2;
-  if (lora) return launch_ragged<false, true>(p, units, s);
-  return swiglu ? launch_ragged<true, false>(p, units, s) : launch_ragged<false, false>(p, units, s);
+  if (low) {
+    if (lora) return launch_ragged<16, false, true>(p, units, s);
+    return swiglu ? launch_ragged<16, true, false>(p, units, s) : launch_ragged<16, false, false>(p, units, s);
+  }
+  if (lora) return launch_ragged<64, false, true>(p, units, s);
+  return swiglu ? launch_ragged<64, true, false>(p, units, s) : launch_ragged<64, false, false>(p, units, s);
 }
 
 }  // namespace tpx
