@@ -47,7 +47,7 @@ constexpr int BOX_ROWS = NT < 32 ? NT : 32;   // rows of x that one load brings 
 // Dynamic shared memory: stages, barriers, the segments' bounds, the tile's rows and adapters.
 template <int NT>
 size_t smem_bytes(int segs) {
-  return 1024 + STAGES * (W_STAGE + X_STAGE<NT>) + (3 * STAGES + 4) * 8 + 16 + ((segs + 4) & ~3) * 4 + 2 * NT * 4;
+  return 1024 + STAGES * (W_STAGE + X_STAGE<NT>) + (4 * STAGES + 4) * 8 + 16 + ((segs + 4) & ~3) * 4 + 2 * NT * 4;
 }
 
 template <int NT, bool SWIGLU, bool LORA>
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   constexpr uint32_t X_BOX = BOX_ROWS<NT> * BK * 2;
   constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
   static_assert(NT % 16 == 0 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM is allocated in powers of two from 32 columns");
-  static_assert(STAGES % 2 == 0, "the bounds behind the 3 * STAGES + 4 barriers start on 16 bytes");
+  static_assert(STAGES % 2 == 0, "the bounds behind the 4 * STAGES + 4 barriers start on 16 bytes");
   static_assert(NT * STG_LD * 4 <= STAGES * (W_STAGE + NT * BK * 2), "the staged output tile reuses the operand stages");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -64,11 +64,11 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
   uint8_t* s_x = smem + STAGES * W_STAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_x + STAGES * X_STAGE);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, rows0 = empty0 + 8 * STAGES;
-  const uint32_t accf = rows0 + 8 * STAGES, drain = accf + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 2);
+  const uint32_t go0 = rows0 + 8 * STAGES, accf = go0 + 8 * STAGES, drain = accf + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   int* s_count = reinterpret_cast<int*>(tmem_slot + 2);            // adapters of this tile
-  int* s_off = reinterpret_cast<int*>(bars + 3 * STAGES + 4) + 4;  // 16-byte aligned
+  int* s_off = reinterpret_cast<int*>(bars + 4 * STAGES + 4) + 4;  // 16-byte aligned
   const int segs = LORA ? p.L : p.E;
   int* s_idx = s_off + ((segs + 4) & ~3);
   int* s_list = s_idx + NT;
@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(rows0 + 8 * s, 128);
+      mbar_init(go0 + 8 * s, 1);
     }
     mbar_init(accf, 1);
     mbar_init(drain, 1);
@@ -218,8 +219,9 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
           tma_gather4(x_dst + 512u * g, &p.tx, k0, max(r.x, 0), max(r.y, 0), max(r.z, 0), max(r.w, 0), fb);
         }
       } else {
-        // two 16-rank steps: B's rows (v of the tokens comes from warps 2..5)
+        // two 16-rank steps: B's rows (v of the tokens comes from warps 2..5, which may fill the slot now)
         if (lane == 0) {
+          mbar_arrive(go0 + 8 * st);
           const int c0 = 2 * (x0 + step - base), nch = min(2, chunks - c0);
           mbar_arrive_expect_tx(fb, nch * 4096u);
           for (int ch = 0; ch < nch; ++ch) {
@@ -286,6 +288,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
       int idx[NT / 16];
 #pragma unroll
       for (int i = 0; i < NT / 16; ++i) idx[i] = r0 + 16 * i < valid ? s_idx[r0 + 16 * i] : -2;
+      uint32_t go_phase = 0;                               // one bit per stage
       for (int step = copy ? 0 : base; step < steps; ++step) {
         const int st = step % STAGES;
         uint4 hi[2], lo[2];
@@ -303,13 +306,18 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
               split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k, hi[ch], lo[ch]);
           }
         }
-        bool ok = mbar_wait_bounded(empty0 + 8 * st, ((step / STAGES) & 1) ^ 1, p.budget, abort_flag);
+        // Rows of x: they follow every use of every slot. v: they may not have, and the parity of `empty` would
+        // say nothing to them; warp 0, which has waited for the slot, lets them go.
+        const bool v_step = LORA && step >= base;
+        bool ok = v_step ? mbar_wait_bounded(go0 + 8 * st, (go_phase >> st) & 1u, p.budget, abort_flag)
+                         : mbar_wait_bounded(empty0 + 8 * st, ((step / STAGES) & 1) ^ 1, p.budget, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (!*abort_flag) record_timeout(p.status, WAIT_PRODUCER_EMPTY);
           *abort_flag = 1u;
           break;
         }
+        if (v_step) go_phase ^= 1u << st;
         const uint32_t x_dst = smem_u32(s_x + st * X_STAGE);
         if (!LORA || step < base) {
           const int k = (kb0 + step) * BK + piece * 8;
@@ -461,6 +469,10 @@ tp_status launch_ragged(const RaggedParams& p, int64_t units, cudaStream_t s) {
 
 }  // namespace
 
+bool lora_takes_pairs(int64_t N, int64_t n, int t) {
+  return N > 64 && 4 * ((N + LORA_TILE - 1) / LORA_TILE) * ((n + 255) / 256) * t >= sm_count();
+}
+
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   RaggedParams p;
   std::memset(&p, 0, sizeof(p));
@@ -470,9 +482,9 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   // Pairs for segments of more than 64 rows on average, if their tiles (256 rows x 256 columns) keep at
   // least half of the pairs busy. x A of 4000 tokens, 8 adapters of rank 64, K = 4096: 23 tiles of pairs,
   // 52 us; 284 CTAs here, 14 us.
-  const int64_t wide_rows = lora ? (g.R + 255) / 256 : g.R / 256 + segs;
-  const int64_t wide_units = wide_rows * ((g.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256)) * (lora ? g.E : 1);
-  const bool pairs = g.R > 64 * segs && 4 * wide_units >= sm_count();
+  const int64_t wide_rows = lora ? (g.R + LORA_TILE - 1) / LORA_TILE : g.R / 256 + segs;
+  const int64_t wide_units = wide_rows * ((g.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
+  const bool pairs = lora ? g.lora_pos != nullptr : g.R > 64 * segs && 4 * wide_units >= sm_count();
   // Low tiles where segments have eight rows or fewer on average (most then fit one).
   const bool low = !pairs && g.R <= 8 * segs;
   const int nt = low ? 16 : 64;
@@ -483,13 +495,13 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the up half of the weights");
   if (g.row_index != nullptr && !encode_bf16_2d(&p.tx, g.x, g.K, g.x_rows, g.K, BK, 1))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
-  if ((g.row_index == nullptr && !encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128)) ||
+  if (((g.row_index == nullptr || lora) && !encode_bf16_2d(&p.tx_box, g.x, g.K, g.x_rows, g.K, BK, 128)) ||
       !encode_bf16_2d(&p.tx_box32, g.x, g.K, g.x_rows, g.K, BK, low ? BOX_ROWS<16> : BOX_ROWS<64>))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the rows");
   if (lora && !encode_bf16_3d(&p.tb, g.lora_b, g.n, g.rank, static_cast<uint64_t>(g.E) * g.L, g.n, 64, 16))
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
   p.x = g.x; p.offsets = g.offsets; p.row_index = g.row_index; p.seg_scale = g.seg_scale;
-  p.y = g.y; p.pre = g.pre; p.h_pre = g.h_pre; p.v = g.v;
+  p.y = g.y; p.pre = g.pre; p.h_pre = g.h_pre; p.v = g.v; p.lora_pos = g.lora_pos; p.lora_lists = g.lora_lists;
   p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
   p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
   p.num_kb = static_cast<int>((g.K + BK - 1) / BK);

@@ -33,6 +33,8 @@ struct RaggedParams {
   uint16_t* pre;              // optional: the products before the activation (SwiGLU: [gate | up], stride 2n)
   const uint16_t* h_pre;      // backward: what the activation was applied to (stride n, SwiGLU 2n)
   const float* v;             // adapters: scale * x A of sorted row i, [N][rank]
+  const int32_t* lora_pos;    // pairs: a token's sorted row if it has an adapter, -1 if not, -2 if it is not named
+  const int32_t* lora_lists;  // pairs: the adapters of every tile of tokens
   int R, x_rows;              // sorted rows, rows of x
   int E, n, K, num_kb, tiles_n;
   int L, rank;                // adapters: their number and rank
@@ -84,10 +86,18 @@ struct RaggedArgs {
   uint16_t* pre;
   const float* seg_scale;
   const float* v;             // adapters, or nullptr
+  const int32_t* lora_pos;    // see RaggedParams; nullptr: the pair kernel is not used
+  const int32_t* lora_lists;
   const uint16_t* lora_b;     // [E][L][rank][n]
   int L, rank;
 };
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
+
+// Adapters on pairs: tiles of LORA_TILE tokens in their own order, each with a list of LORA_LIST ints (its
+// adapters, ascending, behind their number).
+constexpr int LORA_TILE = 256, LORA_LIST = LORA_TILE + 1;
+// Whether a product with adapters takes the pair kernel (which needs lora_pos and lora_lists).
+bool lora_takes_pairs(int64_t N, int64_t n, int t);
 // The same on CTA pairs (row_tiles: how many tiles of 256 rows there can be).
 tp_status ragged_pairs(RaggedParams& p, bool swiglu, bool lora, int64_t row_tiles, cudaStream_t s);
 

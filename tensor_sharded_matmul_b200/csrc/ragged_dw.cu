@@ -228,17 +228,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
     }
   };
   auto relay = [&]() {
-    // Relays, the stages in turn: the loaders' copies are ordered before the tensor cores' reads and passed
+    // Relays, each with slots of its own (see ragged_pair.cu): the loaders' copies are ordered before the tensor cores' reads and passed
     // on to the leader's barrier.
     if (lane == 0) {
-      int st = 0, turn = 2;
+      int st = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < p.units; u += pairs) {
         const int e = u / per_seg;
         const int begin = seg_bound(p.offsets, e, p.R), end = seg_bound(p.offsets, e + 1, p.R);
         for (int r = begin; r < end; r += KB * BK) {
-          if (turn == warp) {
+          if (2 + st % 2 == warp) {
             if (!mbar_wait_bounded(c.rows0 + 8 * st, phase, p.budget, c.abort_flag)) {
               ok = dw_fail(p, c, WAIT_MMA_FULL);
               break;
@@ -247,7 +247,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<GATHER>, 1)
             if (c.rank == 0) mbar_arrive(c.full0 + 8 * st);
             else mbar_arrive_cluster(c.full0_leader + 8 * st);
           }
-          turn ^= 1;
           if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
       }

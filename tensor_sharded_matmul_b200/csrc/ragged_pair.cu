@@ -50,7 +50,7 @@ constexpr unsigned long long DRAIN = 400000000ull;
 
 struct Pair {
   uint8_t *sW, *sX;
-  uint32_t full0, empty0, rows0, accf0, acce0, drain, full0_leader, acce0_leader;
+  uint32_t full0, empty0, rows0, go0, accf0, acce0, drain, full0_leader, acce0_leader;
   volatile uint32_t* abort_flag;
   uint32_t rank;
 };
@@ -93,7 +93,7 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
   if (LORA) {
     rows = p.R;
     first = 0;
-    count = (rows + NT - 1) / NT;
+    count = (rows + LORA_TILE - 1) / LORA_TILE;
     rt = u % count;
     ct = u / count;
     t.e = ct / p.tiles_n;
@@ -110,7 +110,7 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
     rt = local % count;
     ct = local / count;
   }
-  const int step = ((rows + count - 1) / count + 31) & ~31;
+  const int step = LORA ? LORA_TILE : ((rows + count - 1) / count + 31) & ~31;
   t.i0 = first + rt * step;
   t.valid = min(step, rows - rt * step);
   t.n_mma = (t.valid + 31) & ~31;
@@ -134,19 +134,14 @@ __device__ __forceinline__ uint32_t runs_of_half(const RaggedParams& p, int firs
   return runs;
 }
 
-// Adapters that own rows of [i0, i0 + valid): how many, and the first from `a` on.
-__device__ __forceinline__ int count_adapters(const int* off, int L, int i0, int valid, int lane) {
-  int n = 0;
-  for (int a0 = 0; a0 < L; a0 += 32) {
-    const int a = a0 + lane;
-    const bool in = a < L && max(off[a], i0) < min(off[a + 1], i0 + valid);
-    n += __popc(__ballot_sync(0xffffffffu, in));
-  }
-  return n;
+// Whether the stage that begins at k-block kb holds values of v.
+__device__ __forceinline__ bool has_v(const RaggedParams& p, int kb, int total_kb) {
+  return kb + KB > p.num_kb && total_kb > p.num_kb;
 }
-__device__ __forceinline__ int next_adapter(const int* off, int L, int i0, int valid, int a) {
-  while (a < L && !(max(off[a], i0) < min(off[a + 1], i0 + valid))) ++a;
-  return a;
+
+// Adapters: a tile's list as lora_tiles_kernel leaves it, [count, adapters ...] of LIST ints.
+__device__ __forceinline__ const int32_t* tile_list(const RaggedParams& p, const Tile& t) {
+  return p.lora_lists + static_cast<int64_t>(t.i0 / LORA_TILE) * LORA_LIST;
 }
 
 template <bool SWIGLU, bool LORA>
@@ -164,14 +159,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   c.full0 = smem_u32(bars);
   c.empty0 = c.full0 + 8 * STAGES;
   c.rows0 = c.empty0 + 8 * STAGES;
-  c.accf0 = c.rows0 + 8 * STAGES;
+  c.go0 = c.rows0 + 8 * STAGES;
+  c.accf0 = c.go0 + 8 * STAGES;
   c.acce0 = c.accf0 + 16;
   c.drain = c.acce0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 5);
+  static_assert(4 * STAGES + 6 <= 32, "barriers and the TMEM slot");
   c.abort_flag = tmem_slot + 1;
   int* s_off = reinterpret_cast<int*>(bars + 32);
   c.rank = cluster_ctarank();
-  const bool gather = LORA || p.row_index != nullptr;
+  const bool gather = !LORA && p.row_index != nullptr;     // adapters: the tokens' own order
   if (threadIdx.x == 0) {
     prefetch_tmap(&p.tw);
     if (SWIGLU) prefetch_tmap(&p.tw2);
@@ -179,8 +176,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (!gather) prefetch_tmap(&p.tx_box);
     prefetch_tmap(&p.tx_box32);
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(c.full0 + 8 * s, gather ? 3 : 1);    // the leader's TMA thread, and a relay of each CTA
+      mbar_init(c.full0 + 8 * s, gather || LORA ? 3 : 1);   // the leader's TMA thread, and a relay of each CTA
       mbar_init(c.rows0 + 8 * s, 32 * LOADERS);
+      mbar_init(c.go0 + 8 * s, 1);
       mbar_init(c.empty0 + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -231,13 +229,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         runs = runs_of_half(p, row0, min(nh, t.i0 + t.valid - row0), lane, begin);
         x_both += 4096u * __popc(runs);
       }
-      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+      const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
       const int total_kb = p.num_kb + (chunks + 1) / 2;
-      int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
+      int chunk = 0;
       if (lane == 0) {
         for (int kb = 0; kb < total_kb; kb += KB) {
           ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
           if (!ok) break;
+          if (LORA && has_v(p, kb, total_kb)) mbar_arrive(c.go0 + 8 * st);   // the loaders may fill their part
           const uint32_t fb = c.full0_leader + 8 * st;
           uint32_t bytes = 0;
 #pragma unroll
@@ -245,7 +244,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (kb + h < p.num_kb) bytes += 2 * HALF + x_both;
             else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 8192u;
           }
-          if (c.rank == 0) mbar_arrive_expect_tx(c.full0 + 8 * st, bytes);   // of both CTAs
+          if (c.rank == 0) {
+            mbar_arrive_expect_tx(c.full0 + 8 * st, bytes);   // of both CTAs
+            if (LORA && !has_v(p, kb, total_kb)) {            // nothing for the relays
+              mbar_arrive(c.full0 + 8 * st);
+              mbar_arrive(c.full0 + 8 * st);
+            }
+          }
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
             const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
@@ -258,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 tma_load_3d_pair(w + BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? col : col + 64, k0, t.e, fb);
               }
               if (x_bytes == HALF) tma_load_2d_pair(x, &p.tx_box, k0, row0, fb);
-              else if (!LORA)
+              else
                 for (int b = 0; b < static_cast<int>(x_bytes / 4096u); ++b)
                   tma_load_2d_pair(x + 4096u * b, &p.tx_box32, k0, row0 + 32 * b, fb);
 #pragma unroll
@@ -266,10 +271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (runs >> g & 1) tma_load_2d_pair(x + 4096u * g, &p.tx_box32, k0, begin[g], fb);
             } else if (LORA && kb + h < total_kb) {
               const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
-              for (int ch = 0; ch < nch; ++ch) {
-                tma_load_3d_pair(w + ch * 2048u, &p.tb, col, q * 16, t.e * p.L + a, fb);
-                tma_load_3d_pair(w + ch * 2048u + BOX, &p.tb, col + 64, q * 16, t.e * p.L + a, fb);
-                if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+              for (int ch = 0; ch < nch; ++ch, ++chunk) {
+                const int a = ld_s32(tile_list(p, t) + 1 + chunk / per_adapter), r0 = chunk % per_adapter * 16;
+                tma_load_3d_pair(w + ch * 2048u, &p.tb, col, r0, t.e * p.L + a, fb);
+                tma_load_3d_pair(w + ch * 2048u + BOX, &p.tb, col + 64, r0, t.e * p.L + a, fb);
               }
             }
           }
@@ -287,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int u = pair; ok; u += pairs) {
         const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
         if (!t.live) break;
-        const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+        const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
         const int total_kb = p.num_kb + (chunks + 1) / 2;
         const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !p.w_km, false);
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
@@ -412,8 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int q = 0; q < 8; ++q) f[q] *= sc;
           }
           if constexpr (LORA) {
-            const int r = ld_s32(p.row_index + i);
-            if (r >= 0 && r < p.x_rows) store_row8(p, static_cast<int64_t>(t.e) * p.R + r, col, f, up);
+            if (ld_s32(p.lora_pos + i) >= -1) store_row8(p, static_cast<int64_t>(t.e) * p.R + i, col, f, up);
           } else {
             store_row8(p, i, col, f, up);
           }
@@ -425,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-  } else if (gather && warp < RELAY0) {
+  } else if ((gather || LORA) && warp < RELAY0) {
     // Row loaders: eight lanes copy one row's 128 bytes of a k-block. The copies arrive on this CTA's
     // barrier when they have landed.
     const int tid = threadIdx.x - 32 * LOAD0;
@@ -434,107 +438,118 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int v_row = tid >> 1;                        // adapters: two threads build one row of 32 values
     bool waited = false;
     int st = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, go_phase = 0;                  // go_phase: one bit per stage
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
       if (!t.live) break;
       const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
       const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
-      int begin[4];
-      const uint32_t runs = runs_of_half(p, t.i0 + half0, mine, lane, begin);   // come by TMA
       int idx[128 / STEP];
+      if (!LORA) {
+        int begin[4];
+        const uint32_t runs = runs_of_half(p, t.i0 + half0, mine, lane, begin);   // come by TMA
 #pragma unroll
-      for (int i = 0; i < 128 / STEP; ++i) {
-        const int row = r0 + STEP * i;
-        idx[i] = -2;                                   // no row: left as it is (its column is not read)
-        if (row < mine && !(runs >> (row >> 5) & 1)) {
-          const int r = ld_s32(p.row_index + t.i0 + half0 + row);
-          idx[i] = r >= 0 && r < p.x_rows ? r : -1;    // -1: outside x, zeros
-        }
-      }
-      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
-      const int total_kb = p.num_kb + (chunks + 1) / 2;
-      int a = LORA ? next_adapter(s_off, p.L, t.i0, t.valid, 0) : 0, q = 0;
-      for (int kb = 0; kb < total_kb; kb += KB) {
-        // a stage that holds rows of v: they are loaded before its slot is waited for
-        const bool extra = LORA && kb + KB > p.num_kb && total_kb > p.num_kb;
-        uint4 hi[2 * KB], lo[2 * KB];
-        if (extra) {
-          if (!waited) wait_prerequisites();           // v is the kernel before's
-          waited = true;
-#pragma unroll
-          for (int i = 0; i < 2 * KB; ++i) {
-            hi[i] = lo[i] = make_uint4(0, 0, 0, 0);
-            const int chunk = 2 * (kb - p.num_kb) + i;
-            if (chunk < 0 || chunk >= chunks) continue;
-            const int row = t.i0 + half0 + v_row, k0 = q * 16 + (tid & 1) * 8;
-            if (v_row < mine && row >= s_off[a] && row < s_off[a + 1] && k0 < p.rank)
-              split_bf8(p.v + static_cast<int64_t>(row) * p.rank + k0, hi[i], lo[i]);
-            if (++q == per_adapter) { q = 0; a = next_adapter(s_off, p.L, t.i0, t.valid, a + 1); }
+        for (int i = 0; i < 128 / STEP; ++i) {
+          const int row = r0 + STEP * i;
+          idx[i] = -2;                                 // no row: left as it is (its column is not read)
+          if (row < mine && !(runs >> (row >> 5) & 1)) {
+            const int r = ld_s32(p.row_index + t.i0 + half0 + row);
+            idx[i] = r >= 0 && r < p.x_rows ? r : -1;  // -1: outside x, zeros
           }
         }
-        ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
-        if (!ok) break;
+      }
+      if constexpr (LORA) {
+        // Only the stages that hold values of v are theirs. They may be far ahead of the others or behind them,
+        // so that a parity of the stages' own barriers would say nothing: the TMA thread lets them go.
+        const int pos = v_row < mine ? ld_s32(p.lora_pos + t.i0 + half0 + v_row) : -1;   // the token's v, or -1
+        const int chunks = ld_s32(tile_list(p, t)) * per_adapter;
+        const int total_kb = p.num_kb + (chunks + 1) / 2;
+        int chunk = 0;
+        for (int kb = 0; kb < total_kb; kb += KB) {
+          if (has_v(p, kb, total_kb)) {
+            if (!waited) wait_prerequisites();         // v is the kernel before's
+            waited = true;
+            uint4 hi[2 * KB], lo[2 * KB];              // loaded before the slot is waited for
 #pragma unroll
-        for (int h = 0; h < KB; ++h) {
-          uint8_t* x = c.sX + st * OP_STAGE + h * HALF;
-          if (kb + h < p.num_kb) {
+            for (int i = 0; i < 2 * KB; ++i) {
+              hi[i] = lo[i] = make_uint4(0, 0, 0, 0);
+              if (kb + i / 2 < p.num_kb || chunk >= chunks) continue;
+              const int a = ld_s32(tile_list(p, t) + 1 + chunk / per_adapter), k0 = chunk % per_adapter * 16 + (tid & 1) * 8;
+              if (pos >= 0 && pos >= s_off[a] && pos < s_off[a + 1] && k0 < p.rank)
+                split_bf8(p.v + static_cast<int64_t>(pos) * p.rank + k0, hi[i], lo[i]);
+              ++chunk;
+            }
+            ok = warp_wait(p, c, c.go0 + 8 * st, (go_phase >> st) & 1u, WAIT_PRODUCER_EMPTY);
+            if (!ok) break;
+            go_phase ^= 1u << st;
+#pragma unroll
+            for (int h = 0; h < KB; ++h) {
+              if (kb + h < p.num_kb || v_row >= nh) continue;
+              uint8_t* line = c.sX + st * OP_STAGE + h * HALF + v_row * 128;
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch) {
+                const int pc = 2 * ch + (tid & 1);
+                *reinterpret_cast<uint4*>(line + ((pc ^ (v_row & 7)) << 4)) = hi[2 * h + ch];
+                *reinterpret_cast<uint4*>(line + (((pc + 4) ^ (v_row & 7)) << 4)) = lo[2 * h + ch];
+              }
+            }
+            mbar_arrive(c.rows0 + 8 * st);
+          }
+          if (++st == STAGES) st = 0;
+        }
+      } else {
+        for (int kb = 0; kb < p.num_kb; kb += KB) {
+          ok = warp_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+          if (!ok) break;
+#pragma unroll
+          for (int h = 0; h < KB; ++h) {
+            if (kb + h >= p.num_kb) break;
+            const uint32_t x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
             const int k = (kb + h) * BK + piece * 8;
 #pragma unroll
             for (int i = 0; i < 128 / STEP; ++i) {
               const int row = r0 + STEP * i;
               if (idx[i] != -2) {
                 const bool in = k < p.K && idx[i] >= 0;
-                cp_async16(smem_u32(x) + row * 128 + ((piece ^ (row & 7)) << 4),
+                cp_async16(x + row * 128 + ((piece ^ (row & 7)) << 4),
                            in ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x, in ? 16u : 0u);
               }
             }
-          } else if (extra && v_row < nh) {
-            uint8_t* line = x + v_row * 128;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              const int pc = 2 * ch + (tid & 1);
-              *reinterpret_cast<uint4*>(line + ((pc ^ (v_row & 7)) << 4)) = hi[2 * h + ch];
-              *reinterpret_cast<uint4*>(line + (((pc + 4) ^ (v_row & 7)) << 4)) = lo[2 * h + ch];
-            }
           }
-        }
-        if (extra) {
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          mbar_arrive(c.rows0 + 8 * st);
-        } else {
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.rows0 + 8 * st) : "memory");
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
-        if (++st == STAGES) { st = 0; phase ^= 1u; }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (LORA) wait_prerequisites();                    // completes after the kernel before, always
-  } else if (gather) {
-    // Relays, the stages in turn: what the loaders wrote is ordered before the tensor cores' reads and
-    // passed on to the leader's barrier. (The loaders cannot do it themselves: a release to the other CTA
+  } else if (gather || LORA) {
+    // Relays: what the loaders wrote is ordered before the tensor cores' reads and passed on to the leader's
+    // barrier. A slot has one relay, which waits for each of its uses: one that skipped some could take a
+    // phase's parity for the next one's. (The loaders cannot do it themselves: a release to the other CTA
     // waits for every copy that its thread has in flight.)
     const int mine = warp - RELAY0;
-    int st = 0, turn = 0;
-    uint32_t phase = 0;
+    int st = 0;
+    uint32_t used_phase = 0;                           // one bit per stage
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
       if (!t.live) break;
-      const int chunks = LORA ? count_adapters(s_off, p.L, t.i0, t.valid, lane) * per_adapter : 0;
+      const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
       const int total_kb = p.num_kb + (chunks + 1) / 2;
       if (lane == 0) {
         for (int kb = 0; kb < total_kb; kb += KB) {
-          if (turn == mine) {
-            ok = lane_wait(p, c, c.rows0 + 8 * st, phase, WAIT_MMA_FULL);
+          const bool used = !LORA || has_v(p, kb, total_kb);     // a stage without values of v is not passed on
+          if (used && st % RELAYS == mine) {
+            ok = lane_wait(p, c, c.rows0 + 8 * st, (used_phase >> st) & 1u, WAIT_MMA_FULL);
             if (!ok) break;
             fence_proxy_async();
             if (c.rank == 0) mbar_arrive(c.full0 + 8 * st);
             else mbar_arrive_cluster(c.full0_leader + 8 * st);
           }
-          if (++turn == RELAYS) turn = 0;
-          if (++st == STAGES) { st = 0; phase ^= 1u; }
+          if (used) used_phase ^= 1u << st;
+          if (++st == STAGES) st = 0;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);

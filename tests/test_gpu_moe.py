@@ -459,6 +459,9 @@ def _lora_case(N, k, n, t, L, rank, ids, seed, scale=True):
 @pytest.mark.parametrize("N,k,n,t,L,rank", [
     (1, 64, 128, 1, 1, 8), (1, 4096, 256, 2, 4, 16), (7, 136, 72, 1, 3, 24), (64, 264, 512, 4, 32, 16), (65, 200, 400, 2, 70, 8),
     (300, 128, 272, 1, 5, 64), (500, 72, 64, 8, 2, 128), (130, 64, 136, 1, 1024, 16),
+    # pairs (tiles of 256 tokens by 256 columns that fill half of the GPU): partial tiles, an odd number of k-blocks
+    # (a stage of x and v), few and very many adapters in a tile
+    (600, 72, 3584, 16, 3, 24), (520, 136, 4160, 8, 200, 8), (1000, 512, 4096, 8, 1, 128), (257, 1160, 5120, 8, 4, 40),
 ])
 def test_lora(N, k, n, t, L, rank):
     ids = np.random.default_rng(N + L).integers(-1, L + (N > 5), N).astype(np.int32)     # L itself: no adapter
@@ -493,11 +496,12 @@ def test_lora_infinite_values_stay_with_their_token():
     within(got[keep], ref[0][keep], (slack + 2.0 ** -8 * (np.abs(ref[0]) + slack))[keep], "other tokens")
 
 
-@pytest.mark.parametrize("N", [1, 40, 64, 100])
-def test_lora_calls_back_to_back(N):
+@pytest.mark.parametrize("N,n", [(1, 1024), (40, 1024), (64, 1024), (100, 1024), (700, 6144)])
+def test_lora_calls_back_to_back(N, n):
     """Many calls on one stream with nothing between them (each kernel begins beside the one before it), over several
     sets of buffers: every result is the one of a call by itself, bit for bit, and no wait runs out."""
-    k, n, t, L, rank = 2048, 1024, 2, 4, 16
+    k, t, L, rank = 2048, 2, 4, 16
+    nb = tp.tp_lora_ws_bytes(N, rank)
     sets = []
     for seed in range(3):
         d = S.Draw(seed, "cuda")
@@ -505,10 +509,10 @@ def test_lora_calls_back_to_back(N):
         off, tok, _ = M.sort_rows(ids.cpu().numpy()[:, None], L, rest=True)
         sets.append(dict(x=d.normal((N, k)), w=d.normal((t, k, n // t), 0.02), a=d.normal((L, k, rank), 0.02),
                          b=d.normal((t, L, rank, n // t), 0.5), off=dev(off), tok=dev(tok),
-                         ws=torch.empty(N * rank, device="cuda"), y=torch.zeros((t, N, n // t), dtype=torch.bfloat16, device="cuda")))
+                         ws=torch.empty(nb // 4, device="cuda"), y=torch.zeros((t, N, n // t), dtype=torch.bfloat16, device="cuda")))
 
     def call(s):
-        tp.tp_lora_linear(s["x"], N, k, n, t, s["w"], L, rank, s["a"], s["b"], None, s["off"], s["tok"], s["y"], s["ws"], N * rank * 4)
+        tp.tp_lora_linear(s["x"], N, k, n, t, s["w"], L, rank, s["a"], s["b"], None, s["off"], s["tok"], s["y"], s["ws"], nb)
 
     want = []
     for s in sets:

@@ -111,7 +111,8 @@ def test_plan_refusals_and_sizes():
     p(N=0, id=0, o=0, ws=0)
     assert tp.tp_moe_route_ws_bytes(64, 128, 8) == 0 and tp.tp_moe_route_ws_bytes(65, 128, 8) == 128 * 3 * 4
     assert tp.tp_moe_mlp_ws_bytes(1000, 16, 2) == tp.tp_moe_route_ws_bytes(1000, 16, 2) == 16 * 17 * 4
-    assert tp.tp_lora_plan_ws_bytes(128, 7) == (8 * 3 + 128) * 4 and tp.tp_lora_ws_bytes(100, 24) == 9600
+    assert tp.tp_lora_plan_ws_bytes(128, 7) == (8 * 3 + 128) * 4 and tp.tp_lora_ws_bytes(64, 24) == 64 * 24 * 4
+    assert tp.tp_lora_ws_bytes(300, 24) == 300 * 24 * 4 + 300 * 4 + 2 * 257 * 4
     assert tp.tp_moe_route_ws_bytes(-1, 8, 2) == tp.tp_lora_ws_bytes(0, 8) == 0
 
 
