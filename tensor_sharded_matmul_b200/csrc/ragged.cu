@@ -289,22 +289,25 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
 #pragma unroll
       for (int i = 0; i < NT / 16; ++i) idx[i] = r0 + 16 * i < valid ? s_idx[r0 + 16 * i] : -2;
       uint32_t go_phase = 0;                               // one bit per stage
+      uint4 hi[2], lo[2];                                  // the next step's v, on its way while slots are waited for
+      auto fetch_v = [&](int step) {
+        const int c0 = 2 * (x0 + step - base);
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          hi[ch] = lo[ch] = make_uint4(0, 0, 0, 0);
+          if (c0 + ch >= chunks) continue;
+          const int a = s_list[(c0 + ch) / per_adapter];
+          const int j = tid >> 1, k = ((c0 + ch) % per_adapter) * 16 + (tid & 1) * 8;
+          const int i = j >= valid ? -1 : own_order ? s_idx[j] : i0 + j;
+          if (i >= 0 && i >= s_off[a] && i < s_off[a + 1] && k < p.rank)
+            split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k, hi[ch], lo[ch]);
+        }
+      };
       for (int step = copy ? 0 : base; step < steps; ++step) {
         const int st = step % STAGES;
-        uint4 hi[2], lo[2];
-        const int c0 = 2 * (x0 + step - base);
-        if (LORA && step >= base) {                        // loaded before the slot is waited for
-          if (step == base) wait_prerequisites();          // v is the kernel before's
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            hi[ch] = lo[ch] = make_uint4(0, 0, 0, 0);
-            if (c0 + ch >= chunks) continue;
-            const int a = s_list[(c0 + ch) / per_adapter];
-            const int j = tid >> 1, k = ((c0 + ch) % per_adapter) * 16 + (tid & 1) * 8;
-            const int i = j >= valid ? -1 : own_order ? s_idx[j] : i0 + j;
-            if (i >= 0 && i >= s_off[a] && i < s_off[a + 1] && k < p.rank)
-              split_bf8(p.v + static_cast<int64_t>(i) * p.rank + k, hi[ch], lo[ch]);
-          }
+        if (LORA && step == base) {
+          wait_prerequisites();                            // v is the kernel before's
+          fetch_v(step);
         }
         // Rows of x: they follow every use of every slot. v: they may not have, and the parity of `empty` would
         // say nothing to them; warp 0, which has waited for the slot, lets them go.
@@ -340,6 +343,7 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
             *reinterpret_cast<uint4*>(line + (((at + 4) ^ (row & 7)) << 4)) = lo[ch];
           }
           mbar_arrive(rows0 + 8 * st);
+          if (step + 1 < steps) fetch_v(step + 1);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
