@@ -407,7 +407,10 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         for (int q = 0; q < 8; ++q) f[q] *= sc;
       }
       if constexpr (LORA) {
-        if (r >= 0) store_row8(p, static_cast<int64_t>(e) * p.R + (own_order ? j : r), col, f, u);
+        if (r < 0) continue;
+        const int token = own_order ? j : r;
+        if (*s_count > 0) lora_settle8(p, s_off, e, token, own_order ? r : i0 + j, col, f);
+        store_row8(p, static_cast<int64_t>(e) * p.R + token, col, f, u);
       } else {
         store_row8(p, i0 + j, col, f, u);
       }
@@ -506,6 +509,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
     return fail(TP_ECUDA, "cannot encode the TMA descriptor of the adapters");
   p.x = g.x; p.offsets = g.offsets; p.row_index = g.row_index; p.seg_scale = g.seg_scale;
   p.y = g.y; p.pre = g.pre; p.h_pre = g.h_pre; p.v = g.v; p.lora_pos = g.lora_pos; p.lora_lists = g.lora_lists;
+  p.w = g.w; p.lora_b = g.lora_b;
   p.R = static_cast<int>(g.R); p.x_rows = static_cast<int>(g.x_rows);
   p.E = g.E; p.n = static_cast<int>(g.n); p.K = static_cast<int>(g.K);
   p.num_kb = static_cast<int>((g.K + BK - 1) / BK);

@@ -33,6 +33,8 @@ struct RaggedParams {
   uint16_t* pre;              // optional: the products before the activation (SwiGLU: [gate | up], stride 2n)
   const uint16_t* h_pre;      // backward: what the activation was applied to (stride n, SwiGLU 2n)
   const float* v;             // adapters: scale * x A of sorted row i, [N][rank]
+  const uint16_t* w;          // adapters: what tw and tb describe
+  const uint16_t* lora_b;
   const int32_t* lora_pos;    // pairs: a token's sorted row if it has an adapter, -1 if not, -2 if it is not named
   const int32_t* lora_lists;  // pairs: the adapters of every tile of tokens
   int R, x_rows;              // sorted rows, rows of x
@@ -252,6 +254,51 @@ __device__ __forceinline__ void store_row8(const RaggedParams& p, int64_t row, i
   } else {
     st_v4(static_cast<uint16_t*>(p.y) + row * p.n + col, pack_bf8(f));
   }
+}
+
+// Adapters: the matrix instructions multiply the B of every adapter of a tile with all of the tile's tokens, by
+// zeros where it is not theirs, and 0 * inf is NaN. So where a tile with adapters comes out as something that is
+// not finite, its eight columns are summed again from this token's own adapter alone (`sorted` its row of v, or
+// negative). That costs nothing where all is finite; a token whose x holds a NaN is NaN without the sum.
+__device__ __forceinline__ bool not_finite8(const float (&f)[8]) {
+  bool odd = false;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) odd |= !(fabsf(f[q]) < INFINITY);
+  return odd;
+}
+inline __device__ __noinline__ void lora_again8(const RaggedParams& p, const int* off, int e, int64_t token, int sorted, int col, float* f) {
+  const uint16_t* x = p.x + token * p.K;
+  bool nan = false;
+  for (int k = 0; k < p.K; k += 8) {
+    float a[8];
+    unpack_bf8(ld_stream_v4(x + k), a);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) nan |= a[q] != a[q];
+  }
+  float sum[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) sum[q] = nan ? NAN : 0.0f;
+  auto add = [&](float a, const uint16_t* row) {
+    float b[8];
+    unpack_bf8(ld_stream_v4(row), b);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] = fmaf(a, b[q], sum[q]);
+  };
+  for (int k = 0; !nan && k < p.K; ++k) add(bf(ld_u16(x + k)), p.w + (static_cast<int64_t>(e) * p.K + k) * p.n + col);
+  for (int a = 0; !nan && sorted >= 0 && a < p.L; ++a) {
+    if (sorted < off[a] || sorted >= off[a + 1]) continue;
+    const uint16_t* b = p.lora_b + (static_cast<int64_t>(e) * p.L + a) * p.rank * p.n + col;
+    for (int k = 0; k < p.rank; ++k) add(ld_f32(p.v + static_cast<int64_t>(sorted) * p.rank + k), b + static_cast<int64_t>(k) * p.n);
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) f[q] = sum[q];
+}
+__device__ __forceinline__ void lora_settle8(const RaggedParams& p, const int* off, int e, int64_t token, int sorted, int col, float (&f)[8]) {
+  if (!not_finite8(f)) return;
+  float again[8];
+  lora_again8(p, off, e, token, sorted, col, again);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) f[q] = again[q];
 }
 
 }  // namespace tpx

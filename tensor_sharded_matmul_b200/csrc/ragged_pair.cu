@@ -344,6 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
       if (!t.live) break;
       const int col0 = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
+      const bool adapters = LORA && ld_s32(tile_list(p, t)) > 0;
       // h_pre of the group's next chunk is on its way while this one is finished (it comes from DRAM)
       uint4 h0[ITEMS], h1[ITEMS];
       auto fetch_h = [&](int j0) {
@@ -417,7 +418,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int q = 0; q < 8; ++q) f[q] *= sc;
           }
           if constexpr (LORA) {
-            if (ld_s32(p.lora_pos + i) >= -1) store_row8(p, static_cast<int64_t>(t.e) * p.R + i, col, f, up);
+            const int sorted = ld_s32(p.lora_pos + i);
+            if (sorted < -1) continue;
+            if (adapters) lora_settle8(p, s_off, t.e, i, sorted, col, f);
+            store_row8(p, static_cast<int64_t>(t.e) * p.R + i, col, f, up);
           } else {
             store_row8(p, i, col, f, up);
           }

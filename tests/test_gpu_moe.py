@@ -496,6 +496,37 @@ def test_lora_infinite_values_stay_with_their_token():
     within(got[keep], ref[0][keep], (slack + 2.0 ** -8 * (np.abs(ref[0]) + slack))[keep], "other tokens")
 
 
+@pytest.mark.parametrize("N,n,t", [(3, 128, 1), (40, 272, 2), (130, 264, 1), (600, 3584, 16)])
+def test_lora_infinities_of_an_adapter_stay_with_its_tokens(N, n, t):
+    """An infinity and a NaN in one adapter's B reach its own tokens as the formula says, and no other token of
+    the tile that they share; neither does a row of x that is all NaN."""
+    k, L, rank = 72, 3, 24
+    d = S.Draw(N)
+    x, w = d.normal((N, k), 1.0), d.normal((t, k, n // t), 0.1)
+    a, b = d.normal((L, k, rank), 0.1), d.normal((t, L, rank, n // t), 0.5)
+    ids = ((np.arange(N) * 7 + 1) % (L + 1) - 1).astype(np.int32)
+    assert ids[0] == 0 and (N < 40 or ids[1] == -1)
+    size = M.lora(np.abs(f64(x)), np.abs(f64(w)), np.abs(f64(a)), np.abs(f64(b)), None, ids)
+    b[0, 0, 5, 9] = math.inf
+    b[t - 1, 0, rank - 1, 0] = math.nan
+    x[1] = math.nan
+    with np.errstate(invalid="ignore"):
+        ref = M.lora(f64(x), f64(w), f64(a), f64(b), None, ids)
+    off, tok, _ = M.sort_rows(ids[:, None], L, rest=True)
+    y = torch.full((t, N, n // t), MARK, dtype=torch.bfloat16, device="cuda")
+    nb = tp.tp_lora_ws_bytes(N, rank)
+    ws = torch.full((nb // 4,), math.nan, device="cuda")
+    tp.tp_lora_linear(dev(x), N, k, n, t, dev(w), L, rank, dev(a), dev(b), None, dev(off), dev(tok), y, ws, nb)
+    settled()
+    got, good = f64(y), np.isfinite(ref)
+    own = ids == 0
+    own[1] = True
+    assert good[:, ~own].all() and not good.all()
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)])
+    slack = size * ((2 * k + 2 * rank) * 2.0 ** -23 + 2.0 ** -16)
+    within(got[good], ref[good], (slack + 2.0 ** -8 * (np.abs(ref) + slack))[good], "finite")
+
+
 @pytest.mark.parametrize("N,n", [(1, 1024), (40, 1024), (64, 1024), (100, 1024), (700, 6144)])
 def test_lora_calls_back_to_back(N, n):
     """Many calls on one stream with nothing between them (each kernel begins beside the one before it), over several
