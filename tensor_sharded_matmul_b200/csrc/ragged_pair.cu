@@ -110,9 +110,15 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
     rt = local % count;
     ct = local / count;
   }
-  const int step = LORA ? LORA_TILE : ((rows + count - 1) / count + 31) & ~31;
-  t.i0 = first + rt * step;
-  t.valid = min(step, rows - rt * step);
+  if (LORA) {
+    t.i0 = rt * LORA_TILE;
+    t.valid = min(LORA_TILE, rows - t.i0);
+  } else {
+    const int steps = (rows + 31) / 32, each = steps / count, more = steps - each * count;
+    const int begin = 32 * (rt * each + min(rt, more));
+    t.i0 = first + begin;
+    t.valid = min(32 * (each + (rt < more ? 1 : 0)), rows - begin);
+  }
   t.n_mma = (t.valid + 31) & ~31;
   t.n0 = ct * (SWIGLU ? 128 : 256);
   return t;
@@ -209,20 +215,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   int loaded = 0;                                    // warp 0: stages begun
 
   if (warp == 0) {
+    // What a thread executes for one stage is on the critical path (some 5 cycles an instruction), so a
+    // stage of whole k-blocks, which nearly all are, has a loop of its own with little else than its loads.
+    const bool km = p.w_km;
+    const int num_kb = p.num_kb;
+    const uint32_t sw = smem_u32(c.sW), sx = smem_u32(c.sX);
     int st = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
       if (!t.live) break;
-      const int col = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
+      const int col = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128), col2 = SWIGLU ? col : col + 64, e = t.e;
       const int nh = t.n_mma / 2, row0 = t.i0 + static_cast<int>(c.rank) * nh;
       // rows side by side: one box of 128 rows, or (a low tile) as many of 32 as it takes
-      const uint32_t x_bytes = gather ? 0u : nh > 96 ? HALF : static_cast<uint32_t>((nh + 31) / 32) * 4096u;
+      const bool whole = !gather && nh > 96;
+      const int low = gather || whole ? 0 : (nh + 31) / 32;
       // gathered rows: groups that happen to lie side by side come by TMA all the same
       uint32_t runs = 0;
       int begin[4] = {0, 0, 0, 0};
-      uint32_t x_both = 2 * x_bytes;                   // of both CTAs
+      uint32_t x_both = whole ? 2 * HALF : 8192u * low;   // bytes of both CTAs
       if (gather) {
         const int other = t.i0 + static_cast<int>(c.rank ^ 1u) * nh;
         x_both = 4096u * __popc(runs_of_half(p, other, min(nh, t.i0 + t.valid - other), lane, begin));
@@ -230,51 +242,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         x_both += 4096u * __popc(runs);
       }
       const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
-      const int total_kb = p.num_kb + (chunks + 1) / 2;
-      int chunk = 0;
+      const int total_kb = num_kb + (chunks + 1) / 2;
       if (lane == 0) {
-        for (int kb = 0; kb < total_kb; kb += KB) {
-          ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
-          if (!ok) break;
-          if (LORA && has_v(p, kb, total_kb)) mbar_arrive(c.go0 + 8 * st);   // the loaders may fill their part
-          const uint32_t fb = c.full0_leader + 8 * st;
-          uint32_t bytes = 0;
-#pragma unroll
-          for (int h = 0; h < KB; ++h) {
-            if (kb + h < p.num_kb) bytes += 2 * HALF + x_both;
-            else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - p.num_kb)) * 8192u;
+        auto load_kb = [&](int kb, uint32_t w, uint32_t x, uint32_t fb) {
+          const int k0 = kb * BK;
+          if (km) {
+            tma_load_3d_pair(w, &p.tw, k0, col, e, fb);
+          } else {
+            tma_load_3d_pair(w, &p.tw, col, k0, e, fb);
+            tma_load_3d_pair(w + BOX, SWIGLU ? &p.tw2 : &p.tw, col2, k0, e, fb);
           }
-          if (c.rank == 0) {
-            mbar_arrive_expect_tx(c.full0 + 8 * st, bytes);   // of both CTAs
-            if (LORA && !has_v(p, kb, total_kb)) {            // nothing for the relays
-              mbar_arrive(c.full0 + 8 * st);
-              mbar_arrive(c.full0 + 8 * st);
-            }
-          }
-#pragma unroll
-          for (int h = 0; h < KB; ++h) {
-            const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
-            if (kb + h < p.num_kb) {
-              const int k0 = (kb + h) * BK;
-              if (p.w_km) {
-                tma_load_3d_pair(w, &p.tw, k0, col, t.e, fb);
-              } else {
-                tma_load_3d_pair(w, &p.tw, col, k0, t.e, fb);
-                tma_load_3d_pair(w + BOX, SWIGLU ? &p.tw2 : &p.tw, SWIGLU ? col : col + 64, k0, t.e, fb);
-              }
-              if (x_bytes == HALF) tma_load_2d_pair(x, &p.tx_box, k0, row0, fb);
-              else
-                for (int b = 0; b < static_cast<int>(x_bytes / 4096u); ++b)
-                  tma_load_2d_pair(x + 4096u * b, &p.tx_box32, k0, row0 + 32 * b, fb);
+          if (whole) {
+            tma_load_2d_pair(x, &p.tx_box, k0, row0, fb);
+          } else {
+            for (int b = 0; b < low; ++b) tma_load_2d_pair(x + 4096u * b, &p.tx_box32, k0, row0 + 32 * b, fb);
+            if (runs != 0) {
 #pragma unroll
               for (int g = 0; g < 4; ++g)
                 if (runs >> g & 1) tma_load_2d_pair(x + 4096u * g, &p.tx_box32, k0, begin[g], fb);
+            }
+          }
+        };
+        const uint32_t stage_bytes = KB * (2 * HALF + x_both);
+        int kb = 0;
+        for (; kb + KB <= num_kb; kb += KB) {
+          ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+          if (!ok) break;
+          if (c.rank == 0) {
+            mbar_arrive_expect_tx(c.full0 + 8 * st, stage_bytes);     // of both CTAs
+            if (LORA) mbar_arrive_n(c.full0 + 8 * st, 2);             // nothing for the relays
+          }
+#pragma unroll
+          for (int h = 0; h < KB; ++h)
+            load_kb(kb + h, sw + st * OP_STAGE + h * HALF, sx + st * OP_STAGE + h * HALF, c.full0_leader + 8 * st);
+          ++loaded;
+          if (++st == STAGES) { st = 0; phase ^= 1u; }
+        }
+        int chunk = 0;
+        for (; ok && kb < total_kb; kb += KB) {                       // a last odd k-block, and adapters
+          ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
+          if (!ok) break;
+          const bool v = LORA && has_v(p, kb, total_kb);
+          if (v) mbar_arrive(c.go0 + 8 * st);                         // the loaders may fill their part
+          const uint32_t fb = c.full0_leader + 8 * st;
+          uint32_t bytes = 0;
+          for (int h = 0; h < KB; ++h) {
+            if (kb + h < num_kb) bytes += 2 * HALF + x_both;
+            else if (LORA && kb + h < total_kb) bytes += min(2, chunks - 2 * (kb + h - num_kb)) * 8192u;
+          }
+          if (c.rank == 0) {
+            mbar_arrive_expect_tx(c.full0 + 8 * st, bytes);
+            if (LORA && !v) mbar_arrive_n(c.full0 + 8 * st, 2);
+          }
+          for (int h = 0; h < KB; ++h) {
+            const uint32_t w = sw + st * OP_STAGE + h * HALF, x = sx + st * OP_STAGE + h * HALF;
+            if (kb + h < num_kb) {
+              load_kb(kb + h, w, x, fb);
             } else if (LORA && kb + h < total_kb) {
-              const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
+              const int nch = min(2, chunks - 2 * (kb + h - num_kb));
               for (int ch = 0; ch < nch; ++ch, ++chunk) {
                 const int a = ld_s32(tile_list(p, t) + 1 + chunk / per_adapter), r0 = chunk % per_adapter * 16;
-                tma_load_3d_pair(w + ch * 2048u, &p.tb, col, r0, t.e * p.L + a, fb);
-                tma_load_3d_pair(w + ch * 2048u + BOX, &p.tb, col + 64, r0, t.e * p.L + a, fb);
+                tma_load_3d_pair(w + ch * 2048u, &p.tb, col, r0, e * p.L + a, fb);
+                tma_load_3d_pair(w + ch * 2048u + BOX, &p.tb, col + 64, r0, e * p.L + a, fb);
               }
             }
           }
@@ -439,6 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x - 32 * LOAD0;
     constexpr int STEP = LOADERS * 4;                  // rows of one pass
     const int piece = tid & 7, r0 = tid >> 3;
+    const uint32_t line0 = smem_u32(c.sX) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // (STEP is a multiple of 8)
     const int v_row = tid >> 1;                        // adapters: two threads build one row of 32 values
     bool waited = false;
     int st = 0;
@@ -449,17 +479,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!t.live) break;
       const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
       const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
-      int idx[128 / STEP];
+      const uint16_t* src[128 / STEP];                 // this thread's piece of its rows, at k = 0
+      uint32_t mine_bits = 0, in_bits = 0;             // rows that it fetches, and those of them that lie in x (others: zeros)
       if (!LORA) {
         int begin[4];
         const uint32_t runs = runs_of_half(p, t.i0 + half0, mine, lane, begin);   // come by TMA
 #pragma unroll
         for (int i = 0; i < 128 / STEP; ++i) {
-          const int row = r0 + STEP * i;
-          idx[i] = -2;                                 // no row: left as it is (its column is not read)
+          const int row = r0 + STEP * i;               // (no row: left as it is, its column is not read)
+          src[i] = p.x;
           if (row < mine && !(runs >> (row >> 5) & 1)) {
             const int r = ld_s32(p.row_index + t.i0 + half0 + row);
-            idx[i] = r >= 0 && r < p.x_rows ? r : -1;  // -1: outside x, zeros
+            mine_bits |= 1u << i;
+            if (r >= 0 && r < p.x_rows) {
+              in_bits |= 1u << i;
+              src[i] = p.x + static_cast<int64_t>(r) * p.K + piece * 8;
+            }
           }
         }
       }
@@ -509,17 +544,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int h = 0; h < KB; ++h) {
             if (kb + h >= p.num_kb) break;
-            const uint32_t x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
-            const int k = (kb + h) * BK + piece * 8;
+            const uint32_t x = line0 + st * OP_STAGE + h * HALF;
+            const int k0 = (kb + h) * BK;
+            const uint32_t in = k0 + piece * 8 < p.K ? in_bits : 0u;
 #pragma unroll
-            for (int i = 0; i < 128 / STEP; ++i) {
-              const int row = r0 + STEP * i;
-              if (idx[i] != -2) {
-                const bool in = k < p.K && idx[i] >= 0;
-                cp_async16(x + row * 128 + ((piece ^ (row & 7)) << 4),
-                           in ? p.x + static_cast<int64_t>(idx[i]) * p.K + k : p.x, in ? 16u : 0u);
-              }
-            }
+            for (int i = 0; i < 128 / STEP; ++i)
+              if (mine_bits >> i & 1) cp_async16(x + i * STEP * 128, in >> i & 1 ? src[i] + k0 : p.x, in >> i & 1 ? 16u : 0u);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.rows0 + 8 * st) : "memory");
           if (++st == STAGES) { st = 0; phase ^= 1u; }
