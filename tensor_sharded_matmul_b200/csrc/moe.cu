@@ -793,7 +793,11 @@ tp_status tp_moe_mlp_fwd(const uint16_t* x, int64_t N, int64_t h, int64_t F, int
   const int64_t R = N * k;
   if (tp_status st = tp_moe_route(logits, logits_dtype, N, E, k, gate, expert, weight, slot, offsets, row_token, ws, ws_bytes, stream))
     return st;
-  if (tp_status st = tp_ragged_linear(x, N, row_token, offsets, R, E, h, F, act, w_in, z, TP_BF16, h_pre, stream)) return st;
+  RaggedArgs g;                                    // (u is not needed yet: it takes the gathered rows)
+  std::memset(&g, 0, sizeof(g));
+  g.x = x; g.x_rows = N; g.row_index = row_token; g.x_copy = u; g.offsets = offsets; g.R = R; g.E = E; g.K = h; g.n = F;
+  g.w = w_in; g.act = act; g.y = z; g.pre = h_pre;
+  if (tp_status st = ragged_product(g, static_cast<cudaStream_t>(stream))) return st;
   if (tp_status st = tp_ragged_linear(z, R, nullptr, offsets, R, E, F, h, TP_ACT_NONE, w_down, u, TP_BF16, nullptr, stream)) return st;
   return tp_moe_combine(u, TP_BF16, R, weight, slot, N, h, k, y, y_dtype, stream);
 }
@@ -821,9 +825,17 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
   if (tp_status st = tp_moe_route_bwd(logits, logits_dtype, N, E, k, gate, expert, dweight_ws, dlogits, stream)) return st;
   if (tp_status st = tp_ragged_linear_dw(z, R, nullptr, du_ws, offsets, R, E, F, h, dw_down, TP_F32, stream)) return st;
   if (tp_status st = tp_ragged_linear_dx(du_ws, offsets, R, E, F, h, w_down, act, h_pre, dh_ws, stream)) return st;
-  if (tp_status st = tp_ragged_linear_dw(x, N, row_token, dh_ws, offsets, R, E, h, wn, dw_in, TP_F32, stream)) return st;
+  // du is not needed any more: where experts have many rows, x's gathered ones are put side by side there (8192 rows, 8
+  // experts, 4096 x 14336: 1120 us gathered, 850 side by side, 26 the copy; 384 rows an expert: 184 and 193)
+  const bool copy = R >= 512 * static_cast<int64_t>(E);
+  if (copy) {
+    if (tp_status st = gather_rows(x, N, row_token, offsets, E, R, h, du_ws, h, static_cast<cudaStream_t>(stream))) return st;
+  }
+  if (tp_status st = tp_ragged_linear_dw(copy ? du_ws : x, copy ? R : N, copy ? nullptr : row_token, dh_ws, offsets, R, E, h, wn, dw_in,
+                                         TP_F32, stream))
+    return st;
   if (N == 0) return TP_OK;
-  // every row's gradient of x takes the place of du, which is not needed any more
+  // every row's gradient of x takes the place of du
   if (tp_status st = tp_ragged_linear_dx(dh_ws, offsets, R, E, h, wn, w_in, TP_ACT_NONE, nullptr, du_ws, stream)) return st;
   return tp_moe_combine(du_ws, TP_BF16, R, nullptr, slot, N, h, k, dx, dx_dtype, stream);
 }

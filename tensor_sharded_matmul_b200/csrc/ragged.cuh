@@ -39,6 +39,7 @@ struct RaggedParams {
   const int32_t* lora_lists;  // pairs: the adapters of every tile of tokens
   int R, x_rows;              // sorted rows, rows of x
   int E, n, K, num_kb, tiles_n;
+  int tile0;                  // pairs: first of the tiles_n column tiles
   int L, rank;                // adapters: their number and rank
   int split;                  // CTAs along the contraction
   int act;                    // tp_act of the epilogue
@@ -73,7 +74,9 @@ tp_status launch_beside(const char* what, void (*kernel)(P...), unsigned grid, i
 struct RaggedArgs {
   const uint16_t* x;          // [x_rows][K]
   int64_t x_rows;
+  int64_t x_ld;               // pairs, rows side by side: elements between rows (0: K)
   const int32_t* row_index;   // see RaggedParams
+  uint16_t* x_copy;           // room for [R][K], to put gathered rows side by side; or nullptr
   const int32_t* offsets;
   int64_t R;                  // rows of y (adapters: tokens)
   int E;                      // segments (adapters: shards, each over all R rows)
@@ -92,6 +95,7 @@ struct RaggedArgs {
   const int32_t* lora_lists;
   const uint16_t* lora_b;     // [E][L][rank][n]
   int L, rank;
+  int tile0, tiles;           // pairs: some of the column tiles (0, 0: all)
 };
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
 
@@ -100,7 +104,10 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
 constexpr int LORA_TILE = 256, LORA_LIST = LORA_TILE + 1;
 // Whether a product with adapters takes the pair kernel (which needs lora_pos and lora_lists).
 bool lora_takes_pairs(int64_t N, int64_t n, int t);
-// The same on CTA pairs (row_tiles: how many tiles of 256 rows there can be).
+// x[row_index[i]] for every row i of a segment, zeros for an index outside x, to dst + i * ld.
+tp_status gather_rows(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const int32_t* offsets, int E, int64_t R, int64_t K,
+                      uint16_t* dst, int64_t ld, cudaStream_t s);
+// The same on CTA pairs (row_tiles: how many tiles of 256 rows there can be; p.tile0 and p.tiles_n are set).
 tp_status ragged_pairs(RaggedParams& p, bool swiglu, bool lora, int64_t row_tiles, cudaStream_t s);
 
 // Host-side arguments of ragged_dw: dw[e] = x_e^T dy_e for every segment.

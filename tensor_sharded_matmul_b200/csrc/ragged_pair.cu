@@ -120,7 +120,7 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
     t.valid = min(32 * (each + (rt < more ? 1 : 0)), rows - begin);
   }
   t.n_mma = (t.valid + 31) & ~31;
-  t.n0 = ct * (SWIGLU ? 128 : 256);
+  t.n0 = (p.tile0 + ct) * (SWIGLU ? 128 : 256);
   return t;
 }
 
@@ -610,6 +610,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
+// A warp copies one row, four 16-byte pieces a lane in flight.
+__global__ void __launch_bounds__(256) gather_rows_kernel(const uint16_t* x, int x_rows, const int32_t* row_index, const int32_t* offsets,
+                                                          int E, int R, int K, uint16_t* dst, int64_t ld) {
+  const int lane = threadIdx.x % 32;
+  const int i = blockIdx.x * 8 + threadIdx.x / 32;
+  wait_prerequisites();
+  launch_dependents();
+  if (i >= R) return;
+  bool in_segment = false;                             // other rows are left as they were
+  for (int e0 = 0; e0 < E && !in_segment; e0 += 32) {
+    const int e = e0 + lane;
+    in_segment = __any_sync(0xffffffffu, e < E && seg_bound(offsets, e, R) <= i && i < seg_bound(offsets, e + 1, R));
+  }
+  if (!in_segment) return;
+  const int r = ld_s32(row_index + i);
+  const bool in = r >= 0 && r < x_rows;
+  const uint16_t* src = x + static_cast<int64_t>(in ? r : 0) * K;
+  uint16_t* to = dst + i * ld;
+  for (int k0 = lane * 8; k0 < K; k0 += 4 * 256) {
+    uint4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = in && k0 + 256 * q < K ? ld_stream_v4(src + k0 + 256 * q) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (k0 + 256 * q < K) st_v4(to + k0 + 256 * q, v[q]);
+  }
+}
+
 template <bool SWIGLU, bool LORA>
 tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
   static int configured_for[64] = {};
@@ -629,8 +657,13 @@ tp_status launch_pair(const RaggedParams& p, int64_t units, cudaStream_t s) {
 
 }  // namespace
 
+tp_status gather_rows(const uint16_t* x, int64_t x_rows, const int32_t* row_index, const int32_t* offsets, int E, int64_t R, int64_t K,
+                      uint16_t* dst, int64_t ld, cudaStream_t s) {
+  return launch_beside("gather_rows_kernel", gather_rows_kernel, static_cast<unsigned>((R + 7) / 8), 256, 0, s, x, static_cast<int>(x_rows),
+                       row_index, offsets, E, static_cast<int>(R), static_cast<int>(K), dst, ld);
+}
+
 tp_status ragged_pairs(RaggedParams& p, bool swiglu, bool lora, int64_t row_tiles, cudaStream_t s) {
-  p.tiles_n = (p.n + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
   const int64_t units = row_tiles * p.tiles_n * (lora ? p.E : 1);
   if (units > INT32_MAX / 2) return fail(TP_ESHAPE, "too many tiles");
   if (lora) return launch_pair<false, true>(p, units, s);

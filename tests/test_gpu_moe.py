@@ -225,6 +225,52 @@ def test_infinities_stay_in_their_own_rows():
     assert not np.isfinite(got[4]).any() and np.isnan(got[25]).all()
 
 
+@pytest.mark.parametrize("act,out,counts,K,n", [
+    ("swiglu", "bf16", [2300, 0, 1, 4211, 700, 2500], 1000, 2048), ("none", "f32", [9000, 5000, 11500], 1000, 4104),
+    ("gelu", "bf16", [19000, 500, 21000], 264, 4096), ("swiglu", "f32", [3, 300, 260], 136, 2048)])
+def test_gathered_rows_that_are_put_side_by_side(act, out, counts, K, n):
+    """Wide products of many gathered rows copy them to the end of y's own rows first. Results are those of rows
+    that the caller put side by side, bit for bit, and the formula's; rows in front of the segments and behind them
+    are left as they were."""
+    d = S.Draw(len(counts), "cuda")
+    N, front, tail = 3000, 5, 7
+    E, wide = len(counts), 2 * n if act == "swiglu" else n
+    off = front + np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(off[-1]) + tail
+    idx = torch.from_numpy(np.random.default_rng(R).integers(0, N, R).astype(np.int32))
+    idx[front], idx[R - tail - 1], idx[front + 1] = -1, N, idx[front + 2]
+    x, w = d.normal((N, K)), d.normal((E, K, wide), 1 / math.sqrt(K))
+    dt, tt, eps = DT[out]
+    outside = (idx < 0) | (idx >= N)
+    rows = torch.where(outside[:, None].cuda(), torch.zeros((), dtype=x.dtype, device="cuda"), x[idx.clamp(0, N - 1).long().cuda()])
+    ys, pres = [], []
+    for gathered in (True, False):
+        y = torch.full((R, n), MARK, dtype=tt, device="cuda")
+        pre = torch.full((R, wide), MARK, dtype=torch.bfloat16, device="cuda") if act != "none" else None
+        tp.tp_ragged_linear(x if gathered else rows, N if gathered else R, dev(idx) if gathered else None, dev(off), R, E, K, n,
+                            ACT[act], w, y, dt, pre)
+        settled()
+        ys.append(y), pres.append(pre)
+    assert torch.equal(ys[0], ys[1])
+    assert act == "none" or torch.equal(pres[0], pres[1])
+    for keep in (slice(0, front), slice(R - tail, R)):
+        assert (ys[0][keep] == MARK).all()
+    for e in range(E):
+        part = slice(int(off[e]), int(off[e + 1]))
+        a, b = rows[part].double(), w[e].double()
+        h, size = a @ b, a.abs() @ b.abs() * K * 2.0 ** -23
+        if act == "swiglu":
+            g, u = h[:, :n], h[:, n:]
+            s = g * torch.sigmoid(g)
+            ref = s * u
+            slack = 1.2 * size[:, :n] * (u.abs() + size[:, n:]) + (s.abs() + 2.0 ** -18 * g.abs()) * size[:, n:] + 2.0 ** -18 * (g * u).abs()
+        elif act == "gelu":
+            ref, slack = 0.5 * h * (1 + torch.erf(h / math.sqrt(2))), 1.2 * size + 2.0 ** -18 * h.abs()
+        else:
+            ref, slack = h, size
+        assert bool(((ys[0][part].double() - ref).abs() <= slack + eps * (ref.abs() + slack)).all()), e
+
+
 @pytest.mark.parametrize("act", ["none", "gelu", "gelu_tanh", "swiglu"])
 @pytest.mark.parametrize("counts,k,n", [("ragged", 136, 200), ("one row", 64, 2056), ("long", 72, 136), ("very long", 264, 72),
                                         ("many", 40, 104), ("one each", 8, 8)])
@@ -382,6 +428,33 @@ def test_mlp_forward_and_backward(N, h, F, E, k, act, gate, masked):
     if not (gate == "topk" and k == 1):
         assert np.linalg.norm(f64(b["dlogits"]) - ref["dlogits"]) < 5 * 2.0 ** -8 * np.linalg.norm(
             M.gate_softmax(f64(host["logits"]), ref["expert"], gate) * np.abs(ref["dweight"]).max(initial=0) + 1e-30)
+
+
+def test_mlp_of_many_rows_an_expert():
+    """The composite puts gathered rows side by side in buffers that it does not need at that moment; its results are
+    those of the operators called one by one on the rows' indices, bit for bit."""
+    N, h, F, E, k = 2100, 512, 2048, 4, 2
+    b, host, forward, backward = _mlp(N, h, F, E, k, "swiglu", "topk", seed=5, masked=11)
+    R = N * k
+    forward()
+    backward()
+    settled()
+    d = {n: dev(host[n]) for n in ("x", "dy", "w_in", "w_down")}
+    z, u, du = (torch.zeros((R, m), dtype=torch.bfloat16, device="cuda") for m in (F, h, h))
+    pre, dh = (torch.zeros((R, 2 * F), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dweight = torch.zeros((N, k), device="cuda")
+    dw_in = torch.zeros((E, h, 2 * F), device="cuda")
+    tp.tp_ragged_linear(d["x"], N, b["row_token"], b["offsets"], R, E, h, F, tp.TP_ACT_SWIGLU, d["w_in"], z, tp.TP_BF16, pre)
+    tp.tp_ragged_linear(z, R, None, b["offsets"], R, E, F, h, tp.TP_ACT_NONE, d["w_down"], u, tp.TP_BF16, None)
+    tp.tp_moe_combine_bwd(d["dy"], tp.TP_BF16, u, tp.TP_BF16, R, b["weight"], b["slot"], N, h, k, du, dweight)
+    tp.tp_ragged_linear_dx(du, b["offsets"], R, E, F, h, d["w_down"], tp.TP_ACT_SWIGLU, pre, dh)
+    tp.tp_ragged_linear_dw(d["x"], N, b["row_token"], dh, b["offsets"], R, E, h, 2 * F, dw_in, tp.TP_F32)
+    settled()
+    rows = int(b["offsets"][-1])
+    assert rows == R - 11 * k
+    for name, got in (("z", z), ("u", u)):
+        assert torch.equal(b[name][:rows], got[:rows]), name
+    assert torch.equal(b["dw_in"], dw_in)
 
 
 def test_a_captured_step_replays_on_new_routings():
