@@ -337,7 +337,11 @@ tp_status tp_layer_fwd(const uint16_t* x, const uint16_t* const* o, int64_t N, i
  *     matrices are contiguous.
  *   - Sums are binary32 on the tensor cores, whose adds truncate: relative error about
  *     (contraction / 32) * 2^-24 before the one rounding to the output type.
- *   - Results do not depend on launch shape or timing (no atomics), and no call keeps state.
+ *   - Results do not depend on launch shape or timing (no atomics on them), and no call keeps state.
+ *   - Outputs may hold intermediate values until the call's kernels are done (a wide product puts gathered rows
+ *     side by side at the end of y's own rows); no output may overlap an input or another output.
+ *   - Kernels of these calls are launched to begin beside the kernel before them on the stream, and wait for it
+ *     before they read or write anything: results are those of the stream's order.
  * ------------------------------------------------------------------------------------------------ */
 #define TP_MAX_EXPERTS 1024
 #define TP_MAX_TOPK 16
@@ -359,8 +363,8 @@ tp_status tp_moe_route(const void* logits, tp_dtype dtype, int64_t N, int E, int
                        void* stream);
 /* Gradient of the logits ([N, E], dtype of the logits) from dweight fp32 [N, k]. With q the softmax that
  * `gate` names: dl_i = q_i (dw_i - sum_j q_j dw_j), dw_i = 0 for experts that were not chosen (for
- * TOPK, q_i = 0 there too). dweight of a choice that is -1 is not used. The choice itself (and the
- * order of ties) has no gradient. */
+ * TOPK, q_i = 0 there too). dweight of a choice that is -1 is not used; an expert that two choices of a token
+ * name gets the sum of both. The choice itself (and the order of ties) has no gradient. */
 tp_status tp_moe_route_bwd(const void* logits, tp_dtype dtype, int64_t N, int E, int k, tp_gate gate, const int32_t* expert,
                            const float* dweight, void* dlogits, void* stream);
 
@@ -427,7 +431,9 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
  * Low-rank adapters of many requests at once beside a column-parallel projection (serving): for every
  * token i with adapter a = id[i],   y[r][i] = x[i] . w[r] + scale[a] * (x[i] . A[a]) . B[r][a],
  * the shared projection and the adapters' part accumulated together in binary32 and rounded once;
- * x . A is held in binary32 in between and enters the second product to 16 bits of mantissa.
+ * x . A is held in binary32 in between and enters the second product to 16 bits of mantissa. An infinity or a NaN
+ * in one token's x or in one adapter's A or B reaches the outputs of that token or of that adapter's tokens alone
+ * (such outputs take a slower way).
  * ------------------------------------------------------------------------------------------------ */
 /* Plan of a batch, made once and used by every projection of every layer: the tokens sorted by adapter.
  * id int32 [N]; an id outside 0..L-1 (say -1) means no adapter. offsets int32 [L + 1]; row_token int32

@@ -10,6 +10,9 @@
 // counts are scanned per expert (one warp each), and every block places its own tokens. A batch of at
 // most 64 tokens is one block and one launch.
 //
+// Adapters: the same sort, with the tokens that have none behind all others; and for the pair kernel, which takes
+// tokens in their own order, the adapters of every tile of 256 tokens.
+//
 // Combine: y_n = sum_j weight_nj u[slot_nj], bound by reading u: one thread per eight columns, the k
 // rows' loads issued together. Its gradient reads dy and the k rows once, a warp per token.
 #include <cfloat>

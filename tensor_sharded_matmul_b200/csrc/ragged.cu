@@ -5,15 +5,18 @@
 // tcgen05.mma and the segment's rows are its N, which is chosen for each tile in steps of 16. A
 // segment's last tile so costs what its rows cost, and a decode step's few rows need no padding to
 // 128. W as stored ([K][n], n contiguous) is the M-major operand, the rows of x the K-major one; both
-// come by TMA, x's rows four at a time by index (tile::gather4), so that gathered rows are never
-// copied. One CTA computes one tile: warp 0 loads, one thread of warp 1 issues the MMAs, all warps
-// write the output rows.
+// come by TMA: x's rows in boxes where they lie side by side, up to 16 gathered rows four at a time by index
+// (tile::gather4); of more, four warps copy them with cp.async. One CTA computes one tile: warp 0 loads, one
+// thread of warp 1 issues the MMAs, all warps write the output rows. What bounds it: the bytes of W (8 experts of
+// four rows, 4096 x 14336: 0.94 GB in 140 us; two experts of one token, SwiGLU, 0.47 GB in 80 us, where a plain
+// copy's rate would take 72).
 //
 // With few tiles the contraction is split over the CTAs of a cluster. Each leaves its partial tile in
 // its shared memory; the cluster then sums the partials in rank order (no atomics: results do not
 // depend on timing) and writes the rows, each CTA a share of them.
 //
-// Adapters (y = x W + s_a (x A_a) B_a): the rows are the tokens sorted by adapter, v = s_a x A_a comes
+// Adapters (y = x W + s_a (x A_a) B_a): the rows are the tokens sorted by adapter (up to one tile of tokens: in their
+// own order, with zeros where a token has another adapter), v = s_a x A_a comes
 // from a first product over the adapters' segments, and v B_a is accumulated into the same TMEM tile
 // as further k-blocks: 16 ranks of one adapter are one MMA step over the (sixteens of) rows that it owns, with
 // zeros for other rows among them. The second product is launched as a dependent of the first: it

@@ -5,22 +5,27 @@
 // its N, in steps of 32, each CTA holding half of them. A segment of r rows is cut into ceil(r / 256)
 // tiles of nearly equal height, so that its last tile is not a sliver that streams all of W for a few rows.
 //
-// Per CTA: warp 0 loads W (and x where its rows lie side by side: a prompt's tokens mostly do when they are
-// sorted by adapter, an expert's tokens do not) by TMA; warps 10..17 copy gathered rows with
-// cp.async and warps 18, 19 hand them over; one thread of the leader's warp 1 issues the MMAs; warps 2..9
-// turn the accumulator's rows around through shared memory and write whole row pieces while the next tile
-// is multiplied into the other accumulator. A stage holds two 64-deep k-blocks.
+// Per CTA: warp 0 loads W, and x where its rows lie side by side, by TMA; warps 10..17 copy gathered rows with
+// cp.async (adapters: they put the values of v into shared memory) and warps 18, 19 hand them over; one thread
+// of the leader's warp 1 issues the MMAs; warps 2..9 turn the accumulator's rows around through shared memory and
+// write whole row pieces while the next tile is multiplied into the other accumulator. A stage holds two 64-deep
+// k-blocks, three stages fit.
 //
-// Gathered rows, at 8 experts of 1024 rows, K = 4096, n = 14336 (rows side by side: 1379 TFLOP/s): TMA's
-// tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into registers two stages
-// ahead, 897 (more of them in flight were slower: they need lines of the little L1 that is left);
-// cp.async by four warps, 922, by eight, 1089, by sixteen, 1076; with one k-block a stage, 1040.
+// What bounds it: with rows side by side, the MMAs (their thread waits 90 cycles a stage, of 940); 8 experts of
+// 1024 rows, K = 4096, n = 14336, SwiGLU: 1330 us, 1450 TFLOP/s in a burst; under the power cap the clock falls to 1.2..1.6
+// GHz. Before the loading thread had a loop with little else than its loads, its 1500 cycles a stage were the bound
+// (1600 us). (Stages of one k-block, six of them: 1480 us.)
+// Gathered rows (1820 us there): TMA's tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into
+// registers two stages ahead, 897; cp.async by four warps, 922, by eight, 1089, by sixteen, 1076. What remains is the way
+// through a stage: 500 cycles to issue the copies, as many for them to land, and 1430 for the other CTA's release
+// at cluster scope to reach the leader, of 4100 for three stages. Wide products therefore put many gathered rows side
+// by side first (ragged_product).
 //
 // A stage's barrier lives in the leader, which alone announces the bytes of both CTAs' TMA loads (they are
 // equal): a second announcement from the other CTA cost a fifth of the rate (1058 against 1351 TFLOP/s).
 //
-// A wait that runs out is agreed on by the four epilogue warps before any of them leaves, since they meet
-// at a named barrier.
+// A wait that runs out is agreed on by the eight epilogue warps before any of them leaves, since they meet
+// at named barriers.
 #include <cstring>
 
 #include "ragged.cuh"
