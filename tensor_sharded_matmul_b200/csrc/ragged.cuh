@@ -218,7 +218,7 @@ __device__ __forceinline__ void store_backward8(const RaggedParams& p, int64_t r
     unpack_bf8(h1, up);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = 1.0f / (1.0f + __expf(-h[i]));
+      const float s = __fdividef(1.0f, 1.0f + __expf(-h[i]));   // within 2 ulp; 0 where expf overflows
       dg[i] = f[i] * up[i] * (s * (1.0f + h[i] * (1.0f - s)));
       du[i] = f[i] * (h[i] * s);
     }

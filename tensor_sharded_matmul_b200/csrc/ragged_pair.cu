@@ -402,6 +402,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const uint32_t tm = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * 256);
       bool held = true;
       for (int j0 = group * CHUNK; j0 < t.valid; j0 += 2 * CHUNK) {
+        int sorted[ITEMS];                            // adapters: on their way before they are needed
+        if constexpr (LORA) {
+#pragma unroll
+          for (int k = 0; k < ITEMS; ++k) {
+            const int j = j0 + (tid + 128 * k) / GROUPS;
+            sorted[k] = j < t.valid ? ld_s32(p.lora_pos + t.i0 + j) : -2;
+          }
+        }
         uint32_t v[CHUNK];
         tmem_ld16(tm + j0, v);
         tmem_ld_wait();
@@ -452,9 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int q = 0; q < 8; ++q) f[q] *= sc;
           }
           if constexpr (LORA) {
-            const int sorted = ld_s32(p.lora_pos + i);
-            if (sorted < -1) continue;
-            if (adapters) lora_settle8(p, s_off, t.e, i, sorted, col, f);
+            if (sorted[k] < -1) continue;
+            if (adapters) lora_settle8(p, s_off, t.e, i, sorted[k], col, f);
             store_row8(p, static_cast<int64_t>(t.e) * p.R + i, col, f, up);
           } else {
             store_row8(p, i, col, f, up);
