@@ -50,7 +50,7 @@ static_assert(32 * LOADERS == 2 * 128, "two threads build one row of adapter val
 constexpr int STG_LD = 128 + 4;                     // floats between staged rows
 constexpr int CHUNK = 16;                           // rows that a group turns around at a time
 constexpr uint32_t STAGING = 2 * CHUNK * STG_LD * 4;
-constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + STAGING + 256 + (TP_MAX_EXPERTS + 4) * 4;
+constexpr size_t SMEM = 1024 + STAGES * 2 * OP_STAGE + STAGING + 256 + 2 * (TP_MAX_EXPERTS + 4) * 4;
 constexpr unsigned long long DRAIN = 400000000ull;
 
 struct Pair {
@@ -90,39 +90,58 @@ struct Tile {
   bool live;
 };
 
-// Tile u. Token tiles of a segment are neighbours, so that the running pairs share W's columns.
+// first[e]: the units before segment e, for e = 0 .. E, in ascending order whatever the offsets are (a sum beyond
+// what units are counted in is cut off, and what lies behind it has none). One warp.
+__device__ __forceinline__ void count_units(const RaggedParams& p, const int* off, int* first, int lane) {
+  long long base = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    const int rows = e < p.E ? max(off[e + 1] - off[e], 0) : 0;
+    long long inc = static_cast<long long>((rows + NT - 1) / NT) * p.tiles_n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    if (e < p.E) first[e + 1] = static_cast<int>(min(base + inc, static_cast<long long>(INT32_MAX / 2)));
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) first[0] = 0;
+}
+
+// Tile u. Token tiles of a segment are neighbours, so that the running pairs share W's columns. Whole warp.
 template <bool SWIGLU, bool LORA>
-__device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off, int u, int lane) {
+__device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off, const int* first, int u, int lane) {
   Tile t;
-  int rows, count, rt, ct, first;
+  unsigned ct;
   if (LORA) {
-    rows = p.R;
-    first = 0;
-    count = (rows + LORA_TILE - 1) / LORA_TILE;
-    rt = u % count;
+    const unsigned count = (p.R + LORA_TILE - 1) / LORA_TILE;
     ct = u / count;
-    t.e = ct / p.tiles_n;
+    t.i0 = (u - ct * count) * LORA_TILE;
+    t.valid = min(LORA_TILE, p.R - t.i0);
+    t.e = ct / static_cast<unsigned>(p.tiles_n);
     ct -= t.e * p.tiles_n;
     t.live = t.e < p.E;
   } else {
-    const SegTile s = find_seg_tile<NT>(off, p.E, u / p.tiles_n, lane);
-    t.live = s.live;
-    t.e = s.e;
-    first = off[s.e];
-    rows = off[s.e + 1] - first;
-    count = max(s.count, 1);
-    const int local = u - s.before * p.tiles_n;
-    rt = local % count;
+    t.e = 0;
+    t.live = false;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const unsigned hit = __ballot_sync(0xffffffffu, e0 + lane < p.E && first[e0 + lane + 1] > u);
+      if (hit != 0) {
+        t.e = e0 + __ffs(hit) - 1;
+        t.live = true;
+        break;
+      }
+    }
+    if (!t.live) return t;
+    const int begin = off[t.e], rows = off[t.e + 1] - begin;
+    const unsigned count = (rows + NT - 1) / NT, local = u - first[t.e];
     ct = local / count;
-  }
-  if (LORA) {
-    t.i0 = rt * LORA_TILE;
-    t.valid = min(LORA_TILE, rows - t.i0);
-  } else {
-    const int steps = (rows + 31) / 32, each = steps / count, more = steps - each * count;
-    const int begin = 32 * (rt * each + min(rt, more));
-    t.i0 = first + begin;
-    t.valid = min(32 * (each + (rt < more ? 1 : 0)), rows - begin);
+    const int rt = local - ct * count;
+    const int steps = (rows + 31) / 32, each = static_cast<unsigned>(steps) / count, more = steps - each * count;
+    const int from = 32 * (rt * each + min(rt, more));
+    t.i0 = begin + from;
+    t.valid = min(32 * (each + (rt < more ? 1 : 0)), rows - from);
   }
   t.n_mma = (t.valid + 31) & ~31;
   t.n0 = (p.tile0 + ct) * (SWIGLU ? 128 : 256);
@@ -178,6 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   static_assert(4 * STAGES + 6 <= 32, "barriers and the TMEM slot");
   c.abort_flag = tmem_slot + 1;
   int* s_off = reinterpret_cast<int*>(bars + 32);
+  int* s_first = s_off + TP_MAX_EXPERTS + 4;
   c.rank = cluster_ctarank();
   const bool gather = !LORA && p.row_index != nullptr;     // adapters: the tokens' own order
   if (threadIdx.x == 0) {
@@ -208,6 +228,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   launch_dependents();
   const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
+  if (!LORA) {
+    __syncthreads();
+    if (warp == 2) count_units(p, s_off, s_first, lane);
+  }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -229,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
-      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
       if (!t.live) break;
       const int col = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128), col2 = SWIGLU ? col : col + 64, e = t.e;
       const int nh = t.n_mma / 2, row0 = t.i0 + static_cast<int>(c.rank) * nh;
@@ -320,46 +344,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     if (c.rank == 0) {
+      // Descriptors (addresses in units of 16 bytes) of stage 0; a 16-deep step of W is 32 bytes or 16 rows further on.
+      const bool km = p.w_km;
+      const int num_kb = p.num_kb;
+      const uint64_t w0 = smem_desc_sw128(smem_u32(c.sW), km ? 16u : BOX, 1024u), x0 = smem_desc_sw128(smem_u32(c.sX), 16u, 1024u);
+      const uint32_t w_step = km ? 2u : 128u;
       int st = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int u = pair; ok; u += pairs) {
-        const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+        const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
         if (!t.live) break;
         const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
-        const int total_kb = p.num_kb + (chunks + 1) / 2;
-        const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !p.w_km, false);
+        const int total_kb = num_kb + (chunks + 1) / 2;
+        const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !km, false);
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
         if (lane == 0) {
           ok = lane_wait_cluster(p, c, c.acce0 + 8 * acc, acc_phase ^ 1u, WAIT_MMA_ACC_EMPTY);
           tc_fence_after();
-          for (int kb = 0; ok && kb < total_kb; kb += KB) {
+          int kb = 0;
+          for (; ok && kb + KB <= num_kb; kb += KB) {                 // whole stages, as in warp 0
             ok = lane_wait_cluster(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t w = w0 + st * (OP_STAGE >> 4), x = x0 + st * (OP_STAGE >> 4);
 #pragma unroll
+            for (int h = 0; h < KB; ++h)
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                umma_bf16_pair(d, w + h * (HALF >> 4) + k * w_step, x + h * (HALF >> 4) + k * 2, idesc, h != 0 || k != 0 || kb != 0 ? 1u : 0u);
+            mma_issued = true;
+            umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
+            if (++st == STAGES) { st = 0; phase ^= 1u; }
+          }
+          for (; ok && kb < total_kb; kb += KB) {                     // a last odd k-block, and adapters
+            ok = lane_wait_cluster(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
+            if (!ok) break;
+            tc_fence_after();
             for (int h = 0; h < KB; ++h) {
-              const uint32_t w = smem_u32(c.sW + st * OP_STAGE + h * HALF), x = smem_u32(c.sX + st * OP_STAGE + h * HALF);
-              if (kb + h < p.num_kb) {
+              const uint64_t w = w0 + ((st * OP_STAGE + h * HALF) >> 4), x = x0 + ((st * OP_STAGE + h * HALF) >> 4);
+              if (kb + h < num_kb) {
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k) {
-                  const uint64_t ad = p.w_km ? smem_desc_sw128(w + 32u * k, 16u, 1024u) : smem_desc_sw128(w + 2048u * k, BOX, 1024u);
-                  umma_bf16_pair(d, ad, smem_desc_sw128(x + 32u * k, 16u, 1024u), idesc, (kb + h) != 0 || k != 0 ? 1u : 0u);
-                }
+                for (int k = 0; k < BK / 16; ++k) umma_bf16_pair(d, w + k * w_step, x + k * 2, idesc, (kb + h) != 0 || k != 0 ? 1u : 0u);
               } else if (LORA && kb + h < total_kb) {
-                const int nch = min(2, chunks - 2 * (kb + h - p.num_kb));
-                for (int i = 0; i < 2 * nch; ++i) {   // hi and lo of each step against the same rows of B
-                  const int ch = i >> 1, half = i & 1;
-                  umma_bf16_pair(d, smem_desc_sw128(w + 2048u * ch, BOX, 1024u),
-                                 smem_desc_sw128(x + 32u * (ch + 2 * half), 16u, 1024u), idesc, 1u);
-                }
+                const int nch = min(2, chunks - 2 * (kb + h - num_kb));
+                for (int ch = 0; ch < nch; ++ch)      // hi and lo of each step against the same rows of B
+                  for (int half = 0; half < 2; ++half) umma_bf16_pair(d, w + ch * 128, x + (ch + 2 * half) * 2, idesc, 1u);
               }
             }
             mma_issued = true;
             umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
-            if (kb + KB >= total_kb) umma_commit_pair_mc(c.accf0 + 8 * acc, 0x3);
             if (++st == STAGES) { st = 0; phase ^= 1u; }
           }
+          if (ok) umma_commit_pair_mc(c.accf0 + 8 * acc, 0x3);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
@@ -375,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int u = pair;; u += pairs) {
-      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
       if (!t.live) break;
       const int col0 = t.n0 + static_cast<int>(c.rank) * (SWIGLU ? 64 : 128);
       const bool adapters = LORA && ld_s32(tile_list(p, t)) > 0;
@@ -487,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t phase = 0, go_phase = 0;                  // go_phase: one bit per stage
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
-      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
       if (!t.live) break;
       const int nh = t.n_mma / 2, half0 = static_cast<int>(c.rank) * nh;
       const int mine = min(nh, t.valid - half0);       // rows that this CTA fetches (may be <= 0)
@@ -580,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint32_t used_phase = 0;                           // one bit per stage
     bool ok = true;
     for (int u = pair; ok; u += pairs) {
-      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, u, lane);
+      const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
       if (!t.live) break;
       const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
       const int total_kb = p.num_kb + (chunks + 1) / 2;
