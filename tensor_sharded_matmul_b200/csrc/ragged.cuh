@@ -54,9 +54,9 @@ struct RaggedParams {
 // (wait_prerequisites) before it touches global memory, and then lets the next one begin. Back to back
 // such launches hide about 2 us each: the launch and, for the products, barriers and TMEM.
 template <typename... P, typename... A>
-tp_status launch_beside(const char* what, void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
+tp_status launch_beside(const char* what, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

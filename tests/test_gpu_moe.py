@@ -535,6 +535,10 @@ def _lora_case(N, k, n, t, L, rank, ids, seed, scale=True):
     # pairs (tiles of 256 tokens by 256 columns that fill half of the GPU): partial tiles, an odd number of k-blocks
     # (a stage of x and v), few and very many adapters in a tile
     (600, 72, 3584, 16, 3, 24), (520, 136, 4160, 8, 200, 8), (1000, 512, 4096, 8, 1, 128), (257, 1160, 5120, 8, 4, 40),
+    # few tokens: x A token by token (ranks that end inside sixteen, every adapter or one, very long contractions), and
+    # the sizes from which it is a product
+    (1, 4104, 128, 1, 1, 40), (5, 9000, 64, 1, 1024, 8), (64, 1000, 136, 1, 64, 32), (64, 2056, 128, 1, 1, 48), (64, 4096, 72, 1, 2, 24),
+    (3, 200, 64, 1, 2, 264),
 ])
 def test_lora(N, k, n, t, L, rank):
     ids = np.random.default_rng(N + L).integers(-1, L + (N > 5), N).astype(np.int32)     # L itself: no adapter
@@ -600,7 +604,7 @@ def test_lora_infinities_of_an_adapter_stay_with_its_tokens(N, n, t):
     within(got[good], ref[good], (slack + 2.0 ** -8 * (np.abs(ref) + slack))[good], "finite")
 
 
-@pytest.mark.parametrize("N,n", [(1, 1024), (40, 1024), (64, 1024), (100, 1024), (700, 6144)])
+@pytest.mark.parametrize("N,n", [(1, 1024), (3, 1024), (40, 1024), (64, 1024), (100, 1024), (700, 6144)])
 def test_lora_calls_back_to_back(N, n):
     """Many calls on one stream with nothing between them (each kernel begins beside the one before it), over several
     sets of buffers: every result is the one of a call by itself, bit for bit, and no wait runs out."""
