@@ -446,7 +446,7 @@ tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, in
  * [t, L, rank, n/t]; scale fp32 [L] or NULL (ones); y bf16 stacked [t, N, n/t]. row_token must name every
  * token once (a token that it does not name keeps its rows of y; an index outside 0..N-1 is skipped).
  * Adapters of a smaller rank are padded with zeros in A's columns or B's rows. k, n/t and rank multiples
- * of 8, aligned. Workspace tp_lora_ws_bytes (N * rank fp32, and for N > 64 some 8 bytes a token). */
+ * of 8, aligned. Workspace tp_lora_ws_bytes (N * rank fp32, and for N > 64 some 10 bytes a token). */
 size_t tp_lora_ws_bytes(int64_t N, int rank);
 tp_status tp_lora_linear(const uint16_t* x, int64_t N, int64_t k, int64_t n, int t, const uint16_t* w, int L, int rank,
                          const uint16_t* a, const uint16_t* b, const float* scale, const int32_t* offsets,

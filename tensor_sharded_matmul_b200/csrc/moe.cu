@@ -393,15 +393,15 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const void* logits, int6
 }
 
 // ------------------------------------------------------------------ adapters
-// For every tile of LORA_TILE tokens (one block): where each token lies in the sorted order (-1: without an
+// For every tile of `tile` tokens (one block of LORA_TILE threads): where each token lies in the sorted order (-1: without an
 // adapter, -2: not named), and the adapters that the tile has, ascending, behind their number. A block looks
 // through all of row_token: N^2 / 256 reads from L2, 1 us at 4000 tokens, 20 at 65536.
 __global__ void __launch_bounds__(LORA_TILE) lora_tiles_kernel(const int32_t* offsets, const int32_t* row_token, int N, int L,
-                                                               int32_t* pos, int32_t* lists) {
+                                                               int tile, int32_t* pos, int32_t* lists) {
   __shared__ int s_pos[LORA_TILE];
   __shared__ unsigned s_has[(TP_MAX_EXPERTS + 31) / 32];
   __shared__ int s_off[TP_MAX_EXPERTS + 1];
-  const int tid = threadIdx.x, i0 = blockIdx.x * LORA_TILE;
+  const int tid = threadIdx.x, i0 = blockIdx.x * tile;
   begin_beside();
   for (int a = tid; a <= L; a += LORA_TILE) s_off[a] = seg_bound(offsets, a, N);
   for (int w = tid; w < (L + 31) / 32; w += LORA_TILE) s_has[w] = 0u;
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(LORA_TILE) lora_tiles_kernel(const int32_t* of
   __syncthreads();
   for (int i = tid; i < N; i += LORA_TILE) {
     const int t = ld_s32(row_token + i) - i0;
-    if (t < 0 || t >= LORA_TILE || i0 + t >= N) continue;
+    if (t < 0 || t >= tile || i0 + t >= N) continue;
     int lo = 0, hi = L;                            // the segment that holds i, by halving
     while (lo + 1 < hi) {
       const int mid = (lo + hi) / 2;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(LORA_TILE) lora_tiles_kernel(const int32_t* of
     if (a >= 0) atomicOr(s_has + a / 32, 1u << (a % 32));
   }
   __syncthreads();
-  if (i0 + tid < N) pos[i0 + tid] = s_pos[tid];
+  if (tid < tile && i0 + tid < N) pos[i0 + tid] = s_pos[tid];
   if (tid < 32) {
     int32_t* list = lists + static_cast<int64_t>(blockIdx.x) * LORA_LIST;
     int n = 0;
@@ -938,7 +938,7 @@ tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, in
 
 size_t tp_lora_ws_bytes(int64_t N, int rank) {
   if (N <= 0 || rank <= 0 || N > MAX_SIZE) return 0;
-  const size_t tiles = (static_cast<size_t>(N) + LORA_TILE - 1) / LORA_TILE;
+  const size_t tiles = (static_cast<size_t>(N) + LORA_TILE_MIN - 1) / LORA_TILE_MIN;
   // v; beyond one tile of few tokens, every token's place and every tile's adapters
   return static_cast<size_t>(N) * rank * 4 + (N > 64 ? static_cast<size_t>(N) * 4 + tiles * LORA_LIST * 4 : 0);
 }
@@ -965,8 +965,9 @@ tp_status tp_lora_linear(const uint16_t* x, int64_t N, int64_t k, int64_t n, int
   if (lora_takes_pairs(N, n / t, t)) {
     pos = reinterpret_cast<int32_t*>(static_cast<float*>(ws) + N * rank);
     lists = pos + N;
-    if (tp_status st = launch_beside("lora_tiles_kernel", lora_tiles_kernel, static_cast<unsigned>((N + LORA_TILE - 1) / LORA_TILE),
-                                     LORA_TILE, 0, s, offsets, row_token, static_cast<int>(N), L, pos, lists))
+    const int tile = lora_tile(N, n / t, t);
+    if (tp_status st = launch_beside("lora_tiles_kernel", lora_tiles_kernel, static_cast<unsigned>((N + tile - 1) / tile), LORA_TILE, 0, s,
+                                     offsets, row_token, static_cast<int>(N), L, tile, pos, lists))
       return st;
   }
   RaggedArgs g;                                    // v = scale * x A over the adapters' segments, binary32

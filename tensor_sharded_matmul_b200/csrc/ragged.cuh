@@ -41,6 +41,7 @@ struct RaggedParams {
   int E, n, K, num_kb, tiles_n;
   int tile0;                  // pairs: first of the tiles_n column tiles
   int L, rank;                // adapters: their number and rank
+  int lora_tile;              // pairs: tokens of a tile
   int split;                  // CTAs along the contraction
   int act;                    // tp_act of the epilogue
   bool w_km;                  // W stored [E][n][K]
@@ -99,9 +100,11 @@ struct RaggedArgs {
 };
 tp_status ragged_product(const RaggedArgs& g, cudaStream_t s);
 
-// Adapters on pairs: tiles of LORA_TILE tokens in their own order, each with a list of LORA_LIST ints (its
+// Adapters on pairs: tiles of up to LORA_TILE tokens in their own order, each with a list of LORA_LIST ints (its
 // adapters, ascending, behind their number).
-constexpr int LORA_TILE = 256, LORA_LIST = LORA_TILE + 1;
+constexpr int LORA_TILE = 256, LORA_TILE_MIN = 192, LORA_LIST = LORA_TILE + 1;
+// Tokens of a tile for N tokens and t shards of n columns.
+int lora_tile(int64_t N, int64_t n, int t);
 // Whether a product with adapters takes the pair kernel (which needs lora_pos and lora_lists).
 bool lora_takes_pairs(int64_t N, int64_t n, int t);
 // x[row_index[i]] for every row i of a segment, zeros for an index outside x, to dst + i * ld.

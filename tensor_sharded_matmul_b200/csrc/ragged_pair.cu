@@ -87,6 +87,7 @@ __device__ __forceinline__ bool warp_wait(const RaggedParams& p, const Pair& c, 
 
 struct Tile {
   int e, i0, valid, n_mma, n0;
+  int rt;                                             // adapters: which tile of tokens
   bool live;
 };
 
@@ -115,10 +116,11 @@ __device__ __forceinline__ Tile find_tile(const RaggedParams& p, const int* off,
   Tile t;
   unsigned ct;
   if (LORA) {
-    const unsigned count = (p.R + LORA_TILE - 1) / LORA_TILE;
+    const unsigned count = static_cast<unsigned>(p.R + p.lora_tile - 1) / static_cast<unsigned>(p.lora_tile);
     ct = u / count;
-    t.i0 = (u - ct * count) * LORA_TILE;
-    t.valid = min(LORA_TILE, p.R - t.i0);
+    t.rt = u - ct * count;
+    t.i0 = t.rt * p.lora_tile;
+    t.valid = min(p.lora_tile, p.R - t.i0);
     t.e = ct / static_cast<unsigned>(p.tiles_n);
     ct -= t.e * p.tiles_n;
     t.live = t.e < p.E;
@@ -171,7 +173,7 @@ __device__ __forceinline__ bool has_v(const RaggedParams& p, int kb, int total_k
 
 // Adapters: a tile's list as lora_tiles_kernel leaves it, [count, adapters ...] of LIST ints.
 __device__ __forceinline__ const int32_t* tile_list(const RaggedParams& p, const Tile& t) {
-  return p.lora_lists + static_cast<int64_t>(t.i0 / LORA_TILE) * LORA_LIST;
+  return p.lora_lists + static_cast<int64_t>(t.rt) * LORA_LIST;
 }
 
 template <bool SWIGLU, bool LORA>

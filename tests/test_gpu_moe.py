@@ -539,6 +539,8 @@ def _lora_case(N, k, n, t, L, rank, ids, seed, scale=True):
     # the sizes from which it is a product
     (1, 4104, 128, 1, 1, 40), (5, 9000, 64, 1, 1024, 8), (64, 1000, 136, 1, 64, 32), (64, 2056, 128, 1, 1, 48), (64, 4096, 72, 1, 2, 24),
     (3, 200, 64, 1, 2, 264),
+    # tiles of 192 and of 224 tokens
+    (1152, 72, 16384, 16, 8, 16), (4000, 136, 6144, 8, 30, 24),
 ])
 def test_lora(N, k, n, t, L, rank):
     ids = np.random.default_rng(N + L).integers(-1, L + (N > 5), N).astype(np.int32)     # L itself: no adapter
