@@ -268,44 +268,63 @@ __global__ void __launch_bounds__(256) sort_scan_kernel(SortParams p) {
   const int buckets = p.E + p.rest;
   begin_beside();
   if (e >= buckets) return;
+  constexpr int GROUP = 8;
   int32_t* c = p.counts + static_cast<int64_t>(e) * p.blocks;
   int base = 0;
-  for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-    const int b = b0 + lane;
-    const int x = b < p.blocks ? c[b] : 0;
-    int inc = x;
+  for (int b0 = 0; b0 < p.blocks; b0 += 32 * GROUP) {          // loads of a group together: one wait for memory
+    int x[GROUP];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += up;
+    for (int g = 0; g < GROUP; ++g) x[g] = b0 + 32 * g + lane < p.blocks ? c[b0 + 32 * g + lane] : 0;
+#pragma unroll
+    for (int g = 0; g < GROUP; ++g) {
+      const int b = b0 + 32 * g + lane;
+      int inc = x[g];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += up;
+      }
+      if (b < p.blocks) c[b] = base + inc - x[g];
+      base += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (b < p.blocks) c[b] = base + inc - x;
-    base += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (lane == 0) p.counts[static_cast<int64_t>(buckets) * p.blocks + e] = base;
 }
 
 __global__ void __launch_bounds__(256) sort_place_kernel(SortParams p) {
-  extern __shared__ int start[];
+  extern __shared__ int start[];                    // [buckets + 1], then this block's rows before it [buckets]
+  constexpr int MINE = TB * TP_MAX_TOPK / 256;
   const int buckets = p.E + p.rest;
+  int* before = start + buckets + 1;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TB;
+  const int entries = static_cast<int>(p.N - n0 < TB ? p.N - n0 : TB) * p.k;
   begin_beside();
-  for (int e = threadIdx.x; e < buckets; e += blockDim.x)
+  int bucket[MINE], row[MINE];                      // loaded beside the counts
+#pragma unroll
+  for (int m = 0; m < MINE; ++m) {
+    const int i = threadIdx.x + 256 * m;
+    bucket[m] = i < entries ? p.expert[n0 * p.k + i] : 0;
+    row[m] = i < entries ? p.rank[n0 * p.k + i] : -1;
+  }
+  for (int e = threadIdx.x; e < buckets; e += blockDim.x) {
     start[e] = p.counts[static_cast<int64_t>(buckets) * p.blocks + e];
+    before[e] = p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
+  }
   __syncthreads();
   if (threadIdx.x < 32) scan_in_place(start, buckets, threadIdx.x);
   __syncthreads();
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
-  const int entries = static_cast<int>(p.N - n0 < TB ? p.N - n0 : TB) * p.k;
-  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
-    int e = p.expert[n0 * p.k + i], row = p.rank[n0 * p.k + i];
-    if (row >= 0) {
-      if (e < 0 || e >= p.E) e = p.E;               // the rest, behind all
-      row += start[e] + p.counts[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
-      p.row_token[row] = static_cast<int32_t>(n0 + i / p.k);
+#pragma unroll
+  for (int m = 0; m < MINE; ++m) {
+    const int i = threadIdx.x + 256 * m;
+    if (i >= entries) break;
+    if (row[m] >= 0) {
+      const int e = bucket[m] < 0 || bucket[m] >= p.E ? p.E : bucket[m];     // the rest, behind all
+      row[m] += start[e] + before[e];
+      p.row_token[row[m]] = static_cast<int32_t>(n0 + i / p.k);
     }
-    if (p.slot != nullptr) p.slot[n0 * p.k + i] = row;
+    if (p.slot != nullptr) p.slot[n0 * p.k + i] = row[m];
   }
 }
 
@@ -638,7 +657,7 @@ tp_status launch_route_bwd(const void* logits, int64_t N, int E, int k, int gate
 tp_status scan_and_place(const SortParams& p, cudaStream_t s) {
   const int buckets = p.E + p.rest;
   if (tp_status st = launch_beside("sort_scan_kernel", sort_scan_kernel, (buckets + 7) / 8, 256, 0, s, p)) return st;
-  return launch_beside("sort_place_kernel", sort_place_kernel, p.blocks, 256, static_cast<size_t>(buckets + 1) * 4, s, p);
+  return launch_beside("sort_place_kernel", sort_place_kernel, p.blocks, 256, static_cast<size_t>(2 * buckets + 1) * 4, s, p);
 }
 
 int64_t sort_blocks(int64_t N) { return (N + TB - 1) / TB; }
