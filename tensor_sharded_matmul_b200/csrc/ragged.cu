@@ -512,9 +512,11 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
   const int pair_tile = swiglu ? 128 : 256;                         // output columns
   const int64_t pair_tiles = (g.n + pair_tile - 1) / pair_tile;
   // Rows that lie side by side are multiplied faster than gathered ones (8192 rows of uneven segments, K = 4096, n =
-  // 14336, SwiGLU: 1470 against 2030 us), and copying them takes 4 K bytes a row (26 us). So where W has many
-  // columns they are copied first: to x_copy, or else to the end of y's own rows, as long as at least half of y lies
-  // before that (2030 -> 1660 us); the columns that take the copy's place are then multiplied last, from x itself.
+  // 14336, SwiGLU: 1540 against 2030 us), and copying them takes 4 K bytes a row (26 us). So where W has many columns they
+  // are copied first: to x_copy, or else to the end of y's own rows, as long as at least half of y lies before that (1600
+  // us); the columns that take the copy's place are then multiplied last, from x itself. That takes two launches
+  // with their last rounds, and pays from K = 2048 on (16384 rows, n = 4096, SwiGLU: 480 against 501 us; K = 1024, n = 4096:
+  // 171 against 163).
   if (pairs && !lora && g.row_index != nullptr && g.tiles == 0 && g.n * (swiglu ? 2 : 1) >= 4096) {
     RaggedArgs a = g;
     a.row_index = nullptr;
@@ -526,7 +528,7 @@ tp_status ragged_product(const RaggedArgs& g, cudaStream_t s) {
       return ragged_product(a, s);
     }
     const int64_t taken = g.out_f32 ? g.K / 2 : g.K, before = g.n > taken ? (g.n - taken) / pair_tile : 0;
-    if (2 * before >= pair_tiles && wide_rows * (pair_tiles - before) >= 2 * sm_count()) {
+    if (g.K >= 2048 && 2 * before >= pair_tiles && wide_rows * (pair_tiles - before) >= 2 * sm_count()) {
       a.x_ld = g.out_f32 ? 2 * g.n : g.n;
       uint16_t* copy = static_cast<uint16_t*>(g.y) + a.x_ld - g.K;
       a.x = copy;
