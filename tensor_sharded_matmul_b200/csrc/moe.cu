@@ -909,6 +909,7 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
   if (!aligned16(x) || !aligned16(dy) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(h_pre) || !aligned16(z) ||
       !aligned16(u) || !aligned16(du_ws) || !aligned16(dh_ws) || !aligned16(dw_in) || !aligned16(dw_down) || !aligned16(dx))
     return fail(TP_EALIGN, "pointer not 16-byte aligned");
+  if (!aligned4(row_token)) return fail(TP_EALIGN, "pointer not aligned to its elements");
   const int64_t R = N * k, wn = act == TP_ACT_SWIGLU ? 2 * F : F;
   // combine -> down (both gradients) -> activation (in the down product's epilogue) -> up (both) -> tokens
   if (tp_status st = tp_moe_combine_bwd(dy, TP_BF16, u, TP_BF16, R, weight, slot, N, h, k, du_ws, dweight_ws, stream)) return st;

@@ -130,3 +130,19 @@ def test_mlp_refusals_and_empty_calls():
     _linear(R=0, x=0, x_rows=0, index=None, offsets=0, w=0, y=0)
     _route(N=0, logits=0, expert=0, ws=0, ws_bytes=0)
     _lora(N=0, x=0, a=0, ws=0, ws_bytes=0)
+
+
+_BWD = ("x", "dy", "N", "h", "F", "E", "k", "gate", "act", "logits", "logits_dtype", "w_in", "w_down", "expert", "weight", "slot",
+        "offsets", "row_token", "h_pre", "z", "u", "du_ws", "dh_ws", "dweight_ws", "dw_in", "dw_down", "dx", "dx_dtype", "dlogits")
+
+
+def _mlp_bwd(**kw):
+    a = dict({n: FAKE for n in _BWD}, N=4, h=64, F=64, E=8, k=2, gate=tp.TP_GATE_TOPK, act=tp.TP_ACT_GELU, logits_dtype=tp.TP_F32,
+             dx_dtype=tp.TP_F32)
+    a.update(kw)
+    tp.tp_moe_mlp_bwd(*[a[n] for n in _BWD], 0)
+
+
+@pytest.mark.parametrize("N", [4, 4096])           # few rows an expert; many, which are put side by side
+def test_mlp_bwd_refuses_a_row_token_off_its_elements(N):
+    _expect(tp.TP_EALIGN, lambda: _mlp_bwd(N=N, row_token=FAKE + 2))
