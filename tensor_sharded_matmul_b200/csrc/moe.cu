@@ -901,6 +901,8 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
   if (tp_status st = check_route(N, E, k, gate, logits_dtype)) return st;
   if (tp_status st = check_ragged(N, nullptr, N, E, h, F)) return st;
   if (!valid_act(act) || !valid_dtype(dx_dtype)) return fail(TP_EINVAL, "bad activation or dtype");
+  const int64_t R = N * k, wn = act == TP_ACT_SWIGLU ? 2 * F : F;
+  if (wn > MAX_SIZE) return fail(TP_ESHAPE, "size too large");
   if (N > 0 && (!x || !dy || !logits || !w_in || !w_down || !expert || !weight || !slot || !row_token || !z || !u || !du_ws ||
                 !dh_ws || !dweight_ws || !dx || !dlogits))
     return fail(TP_EINVAL, "null pointer");
@@ -909,8 +911,10 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
   if (!aligned16(x) || !aligned16(dy) || !aligned16(w_in) || !aligned16(w_down) || !aligned16(h_pre) || !aligned16(z) ||
       !aligned16(u) || !aligned16(du_ws) || !aligned16(dh_ws) || !aligned16(dw_in) || !aligned16(dw_down) || !aligned16(dx))
     return fail(TP_EALIGN, "pointer not 16-byte aligned");
-  if (!aligned4(row_token)) return fail(TP_EALIGN, "pointer not aligned to its elements");
-  const int64_t R = N * k, wn = act == TP_ACT_SWIGLU ? 2 * F : F;
+  const uintptr_t logit_mask = logits_dtype == TP_F32 ? 3u : 1u;
+  if (!aligned4(expert) || !aligned4(weight) || !aligned4(slot) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(dweight_ws) ||
+      (reinterpret_cast<uintptr_t>(logits) & logit_mask) || (reinterpret_cast<uintptr_t>(dlogits) & logit_mask))
+    return fail(TP_EALIGN, "pointer not aligned to its elements");
   // combine -> down (both gradients) -> activation (in the down product's epilogue) -> up (both) -> tokens
   if (tp_status st = tp_moe_combine_bwd(dy, TP_BF16, u, TP_BF16, R, weight, slot, N, h, k, du_ws, dweight_ws, stream)) return st;
   if (tp_status st = tp_moe_route_bwd(logits, logits_dtype, N, E, k, gate, expert, dweight_ws, dlogits, stream)) return st;

@@ -146,3 +146,17 @@ def _mlp_bwd(**kw):
 @pytest.mark.parametrize("N", [4, 4096])           # few rows an expert; many, which are put side by side
 def test_mlp_bwd_refuses_a_row_token_off_its_elements(N):
     _expect(tp.TP_EALIGN, lambda: _mlp_bwd(N=N, row_token=FAKE + 2))
+
+
+@pytest.mark.parametrize("status,kw", [
+    *[(tp.TP_EALIGN, {n: FAKE + 2}) for n in ("expert", "weight", "slot", "offsets", "dweight_ws", "logits", "dlogits")],
+    (tp.TP_EALIGN, dict(logits=FAKE + 1, logits_dtype=tp.TP_BF16)), (tp.TP_EALIGN, dict(dlogits=FAKE + 1, logits_dtype=tp.TP_BF16)),
+    (tp.TP_ESHAPE, dict(act=tp.TP_ACT_SWIGLU, F=(1 << 28) + 8)),       # its 2 F columns are too many
+])
+def test_mlp_bwd_refuses_before_it_launches(status, kw):
+    _expect(status, lambda: _mlp_bwd(**kw))
+
+
+def test_mlp_bwd_of_no_tokens_checks_what_it_writes():
+    _expect(tp.TP_EALIGN, lambda: _mlp_bwd(N=0, offsets=FAKE + 2))
+    _expect(tp.TP_ESHAPE, lambda: _mlp_bwd(N=0, act=tp.TP_ACT_SWIGLU, F=(1 << 28) + 8))
