@@ -317,6 +317,12 @@ __device__ __forceinline__ int ld_s32(const int32_t* p) {
   asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
+// As ld_s32, from L2 whatever this SM's L1 holds.
+__device__ __forceinline__ int ld_gpu_s32(const int32_t* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 __device__ __forceinline__ float ld_f32(const float* p) {
   float v;
   asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));

@@ -226,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (!LORA) wait_prerequisites();                   // as in ragged.cu
+  wait_prerequisites();                              // up to here beside the kernel before, from here the next one beside this
   launch_dependents();
   const int segs = LORA ? p.L : p.E;
   for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
@@ -521,7 +521,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int piece = tid & 7, r0 = tid >> 3;
     const uint32_t line0 = smem_u32(c.sX) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // (STEP is a multiple of 8)
     const int v_row = tid >> 1;                        // adapters: two threads build one row of 32 values
-    bool waited = false;
     int st = 0;
     uint32_t phase = 0, go_phase = 0;                  // go_phase: one bit per stage
     bool ok = true;
@@ -558,8 +557,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int chunk = 0;
         for (int kb = 0; kb < total_kb; kb += KB) {
           if (has_v(p, kb, total_kb)) {
-            if (!waited) wait_prerequisites();         // v is the kernel before's
-            waited = true;
             uint4 hi[2 * KB], lo[2 * KB];              // loaded before the slot is waited for
 #pragma unroll
             for (int i = 0; i < 2 * KB; ++i) {
@@ -608,7 +605,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (LORA) wait_prerequisites();                    // completes after the kernel before, always
   } else if (gather || LORA) {
     // Relays: what the loaders wrote is ordered before the tensor cores' reads and passed on to the leader's
     // barrier. A slot has one relay, which waits for each of its uses: one that skipped some could take a
