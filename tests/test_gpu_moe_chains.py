@@ -10,7 +10,7 @@ import torch
 
 import synthetic as S
 import tensor_sharded_matmul_b200 as tp
-from test_gpu_moe import settled
+from test_gpu_moe import _mlp, dev, plan_of, settled
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,95 @@ def test_lora_of_changing_batches(N, n, last):
     settled()
     for i, y in enumerate(ys):
         assert same(y, want[i % 3]), i
+
+
+@pytest.mark.parametrize("rows,k,n", [
+    (1, 1024, 512), (20, 1024, 512), (64, 1024, 512), (300, 1024, 512),
+    (300, 2048, 1024),                                   # pairs, gathered rows
+    (1000, 2048, 4096),                                  # pairs, gathered rows that are put side by side first
+])
+def test_products_over_shared_buffers(rows, k, n):
+    """Up (gathered, SwiGLU), down, both gradients of down: each reads what the call before it wrote."""
+    E, N, rounds = 4, 64, 8
+    d = S.Draw(rows + n, "cuda")
+    w1, w2 = d.normal((E, k, 2 * n), 1 / math.sqrt(k)), d.normal((E, n, k), 1 / math.sqrt(n))
+    cases = []
+    for i in range(3):
+        counts = [rows, rows, rows, rows]
+        counts[i], counts[(i + 1) % E] = 2 * rows - rows // 2, rows // 2
+        off, idx, R = plan_of(counts, N, rows + i)
+        cases.append((d.normal((N, k)), dev(off), dev(idx)))
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+
+    def buffers():
+        return dict(x=torch.empty((N, k), **bf), off=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                    idx=torch.empty(R, dtype=torch.int32, device="cuda"), z=torch.empty((R, n), **bf), u=torch.empty((R, k), **bf),
+                    pre=torch.empty((R, 2 * n), **bf), dh=torch.empty((R, 2 * n), **bf), dw=torch.empty((E, n, k), device="cuda"))
+
+    def chain(o, x, off, idx, check=lambda: None):
+        for name in ("z", "u", "pre", "dh", "dw"):
+            o[name].fill_(NAN)
+        o["x"].copy_(x), o["off"].copy_(off), o["idx"].copy_(idx)
+        check()
+        tp.tp_ragged_linear(o["x"], N, o["idx"], o["off"], R, E, k, n, tp.TP_ACT_SWIGLU, w1, o["z"], tp.TP_BF16, o["pre"])
+        check()
+        tp.tp_ragged_linear(o["z"], R, None, o["off"], R, E, n, k, tp.TP_ACT_NONE, w2, o["u"], tp.TP_BF16)
+        check()
+        tp.tp_ragged_linear_dx(o["u"], o["off"], R, E, n, k, w2, tp.TP_ACT_SWIGLU, o["pre"], o["dh"])
+        check()
+        tp.tp_ragged_linear_dw(o["z"], R, None, o["u"], o["off"], R, E, n, k, o["dw"], tp.TP_F32)
+        check()
+        return [o[name].clone() for name in ("z", "u", "pre", "dh", "dw")]
+
+    want = [chain(buffers(), *c, check=settled) for c in cases]
+    for w in want:
+        assert not any(v.isnan().any() for v in w)
+    shared = buffers()
+    got = [chain(shared, *cases[i % 3]) for i in range(rounds)]
+    settled()
+    for i, g in enumerate(got):
+        assert all(same(a, b) for a, b in zip(g, want[i % 3])), i
+
+
+KEPT = ("h_pre", "z", "u", "y", "du", "dh", "dweight", "dw_in", "dw_down", "dx", "dlogits", "weight")
+OUT = ("y", "dx", "dw_in", "dw_down", "dlogits", "weight", "offsets")
+
+
+@pytest.mark.parametrize("N,h,F,E", [(7, 136, 72, 6), (200, 128, 96, 6), (2100, 512, 2048, 4)])
+def test_mlp_over_shared_buffers(N, h, F, E):
+    """Forward and backward of other tokens and logits each time, on one stream and on two at once."""
+    runs = [_mlp(N, h, F, E, 2, "swiglu", "topk", seed=N + i, masked=i) for i in range(3)]
+    inputs = [{n: b[n].clone() for n in ("x", "logits", "dy")} for b, _, _, _ in runs]
+    for b, _, _, _ in runs[1:]:
+        for n in ("w_in", "w_down"):
+            b[n].copy_(runs[0][0][n])
+    want = []
+    for b, _, forward, backward in runs:
+        for n in KEPT:
+            b[n].fill_(NAN)
+        settled()
+        forward(), settled()
+        backward(), settled()
+        want.append({n: b[n].clone() for n in OUT})
+        assert not any(v.isnan().any() for v in want[-1].values())
+
+    def step(run, i, stream):
+        b, _, forward, backward = run
+        for n in KEPT:
+            b[n].fill_(NAN)
+        for n, v in inputs[i].items():
+            b[n].copy_(v)
+        forward(stream), backward(stream)
+        return {n: b[n].clone() for n in OUT}
+
+    got = [(i % 3, step(runs[0], i % 3, None)) for i in range(7)]
+    settled()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(6):
+        for j, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(((i + j) % 3, step(runs[j], (i + j) % 3, s)))
+    settled()
+    for at, (i, g) in enumerate(got):
+        for n in OUT:
+            assert same(g[n], want[i][n]), (at, n)
