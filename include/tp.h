@@ -446,7 +446,8 @@ tp_status tp_lora_plan(const int32_t* id, int64_t N, int L, int32_t* offsets, in
                        void* stream);
 /* x bf16 [N, k]; w bf16 stacked [t, k, n/t] as in tp_column_linear; A bf16 [L, k, rank]; B bf16
  * [t, L, rank, n/t]; scale fp32 [L] or NULL (ones); y bf16 stacked [t, N, n/t]. row_token must name every
- * token once (a token that it does not name keeps its rows of y; an index outside 0..N-1 is skipped).
+ * token once (a token that it does not name keeps its rows of y; an index outside 0..N-1 is skipped). offsets as of the
+ * ragged products: a caller's own need not ascend, as long as segments do not overlap.
  * Adapters of a smaller rank are padded with zeros in A's columns or B's rows. k, n/t and rank multiples
  * of 8, aligned. Workspace tp_lora_ws_bytes (N * rank fp32, and for N > 64 some 10 bytes a token). */
 size_t tp_lora_ws_bytes(int64_t N, int rank);

@@ -412,6 +412,18 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const void* logits, int6
 }
 
 // ------------------------------------------------------------------ adapters
+// The segment of sorted row i among L with clamped bounds `off`, -1 if it lies in none: by halving where the bounds ascend,
+// as a plan's do, or else by trying each (a segment that ends before it begins is empty, wherever the next one begins).
+__device__ __forceinline__ int segment_of(const int* off, int L, int i, bool ascending) {
+  int lo = 0, hi = ascending ? L : 0;
+  while (lo + 1 < hi) {
+    const int mid = (lo + hi) / 2;
+    if (off[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  while (!ascending && lo + 1 < L && !(off[lo] <= i && i < off[lo + 1])) ++lo;
+  return off[lo] <= i && i < off[lo + 1] ? lo : -1;
+}
 // For every tile of `tile` tokens (one block of LORA_TILE threads): where each token lies in the sorted order (-1: without an
 // adapter, -2: not named), and the adapters that the tile has, ascending, behind their number. A block looks
 // through all of row_token: N^2 / 256 reads from L2, 1 us at 4000 tokens, 20 at 65536.
@@ -426,16 +438,13 @@ __global__ void __launch_bounds__(LORA_TILE) lora_tiles_kernel(const int32_t* of
   for (int w = tid; w < (L + 31) / 32; w += LORA_TILE) s_has[w] = 0u;
   s_pos[tid] = -2;
   __syncthreads();
+  bool up = true;
+  for (int a = tid; a < L; a += LORA_TILE) up = up && s_off[a] <= s_off[a + 1];
+  const bool ascending = __syncthreads_and(up);
   for (int i = tid; i < N; i += LORA_TILE) {
     const int t = ld_s32(row_token + i) - i0;
     if (t < 0 || t >= tile || i0 + t >= N) continue;
-    int lo = 0, hi = L;                            // the segment that holds i, by halving
-    while (lo + 1 < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s_off[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const int a = i >= s_off[lo] && i < s_off[lo + 1] ? lo : -1;
+    const int a = segment_of(s_off, L, i, ascending);
     s_pos[t] = a >= 0 ? i : -1;
     if (a >= 0) atomicOr(s_has + a / 32, 1u << (a % 32));
   }
