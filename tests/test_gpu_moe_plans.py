@@ -45,3 +45,37 @@ def test_lora_with_a_callers_own_plan(N, n, t, form):
     got = f64(y)
     within(got[:, ~unnamed], ref[:, ~unnamed], (slack + 2.0 ** -8 * (np.abs(ref) + slack))[:, ~unnamed], form)
     assert (got[:, unnamed] == MARK).all()
+
+
+def test_lora_of_very_many_tokens():
+    """Every token's place and every tile's adapters, far beyond one tile; some places are not named and hold rubbish."""
+    N, k, n, L, rank = 70001, 64, 512, 300, 8
+    d = S.Draw(3, "cuda")
+    x, w, a, b = d.normal((N, k)), d.normal((1, k, n), 0.1), d.normal((L, k, rank), 0.1), d.normal((1, L, rank, n), 0.5)
+    ids = torch.randint(-1, L + 2, (N,), generator=d.gen, device="cuda", dtype=torch.int32)
+    off, tok = torch.full((L + 1,), -9, dtype=torch.int32, device="cuda"), torch.full((N,), -9, dtype=torch.int32, device="cuda")
+    pb, nb = tp.tp_lora_plan_ws_bytes(N, L), tp.tp_lora_ws_bytes(N, rank)
+    tp.tp_lora_plan(ids, N, L, off, tok, torch.empty(pb, dtype=torch.uint8, device="cuda"), pb)
+    lost = tok[::5003].clone().long()
+    tok[::5003] = -1
+    for rubbish in (0, 12345, -1):                       # what the workspace holds before
+        ws = torch.full((nb // 4,), rubbish, dtype=torch.int32, device="cuda")
+        y = torch.full((1, N, n), MARK, dtype=torch.bfloat16, device="cuda")
+        tp.tp_lora_linear(x, N, k, n, 1, w, L, rank, a, b, None, off, tok, y, ws, nb)
+        settled()
+        assert (y[0, lost] == MARK).all()
+        mine = (ids >= 0) & (ids < L)
+        at = torch.where(mine, ids, 0).long()
+        bad = 0
+        for c in range(0, N, 10000):
+            part = slice(c, c + 10000)
+            A, B, X = a[at[part]].double(), b[0, at[part]].double(), x[part].double()
+            A[~mine[part]] = 0
+            v, sv = (torch.einsum("nk,nkr->nr", p, q) for p, q in ((X, A), (X.abs(), A.abs())))
+            ref = X @ w[0].double() + torch.einsum("nr,nrm->nm", v, B)
+            slack = (X.abs() @ w[0].double().abs() + torch.einsum("nr,nrm->nm", sv, B.abs())) * ((2 * k + 2 * rank) * 2.0 ** -23 + 2.0 ** -16)
+            off_by = (y[0, part].double() - ref).abs() > slack + 2.0 ** -8 * (ref.abs() + slack)
+            gone = lost[(lost >= c) & (lost < c + 10000)] - c
+            off_by[gone] = False
+            bad += int(off_by.sum())
+        assert bad == 0
