@@ -372,7 +372,7 @@ tp_status tp_moe_route_bwd(const void* logits, tp_dtype dtype, int64_t N, int E,
 
 /* Product grouped by expert: y[i] = act(x[row_index[i]] . w[e]) for every row i of every expert e.
  *   x          bf16 [x_rows, k]; row_index int32 [R] (NULL: row i of x itself, x_rows >= R). An index
- *              outside 0..x_rows-1 reads as a row of zeros; an index may repeat.
+ *              outside 0..x_rows-1 reads as a row of zeros (NaN where w[e] holds an infinity); an index may repeat.
  *   w          bf16 [E, k, n] ([E, k, 2n] = [gate | up] for SWIGLU)
  *   y          [R, n], y_dtype fp32 or bf16
  *   pre        optional bf16 output, what act is applied to: [R, n] ([R, 2n] for SWIGLU); NULL for

@@ -227,7 +227,14 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
         __syncwarp();
         for (int g = lane; g < groups; g += 32) {
           const int4 r = *reinterpret_cast<const int4*>(s_idx + 4 * g);
-          tma_gather4(x_dst + 512u * g, &p.tx, k0, max(r.x, 0), max(r.y, 0), max(r.z, 0), max(r.w, 0), fb);
+          if ((r.x | r.y | r.z | r.w) >= 0) {
+            tma_gather4(x_dst + 512u * g, &p.tx, k0, r.x, r.y, r.z, r.w, fb);
+          } else {                                         // rows outside x by themselves, from behind x: TMA's zeros
+            for (int q = 0; q < 4; ++q) {
+              const int row = s_idx[4 * g + q];
+              tma_load_2d(x_dst + 512u * g + 128u * q, &p.tx, k0, row >= 0 ? row : p.x_rows, fb);
+            }
+          }
         }
       } else {
         // two 16-rank steps: B's rows (v of the tokens comes from warps 2..5, which may fill the slot now)
@@ -407,18 +414,14 @@ __global__ void __launch_bounds__(THREADS) ragged_kernel(const __grid_constant__
           }
         }
       }
-      const int r = s_idx[j];
-      if (r < 0) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = u[q] = 0.0f;
-      }
       if (p.seg_scale != nullptr) {
         const float sc = ld_f32(p.seg_scale + e);
 #pragma unroll
         for (int q = 0; q < 8; ++q) f[q] *= sc;
       }
       if constexpr (LORA) {
-        if (r < 0) continue;
+        const int r = s_idx[j];
+        if (r < 0) continue;                           // no token
         const int token = own_order ? j : r;
         if (*s_count > 0) lora_settle8(p, s_off, e, token, own_order ? r : i0 + j, col, f);
         store_row8(p, static_cast<int64_t>(e) * p.R + token, col, f, u);

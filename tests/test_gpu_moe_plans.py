@@ -79,3 +79,39 @@ def test_lora_of_very_many_tokens():
             off_by[gone] = False
             bad += int(off_by.sum())
         assert bad == 0
+
+
+@pytest.mark.parametrize("counts,K,n,act", [
+    ([3, 0, 1], 72, 136, "none"), ([40, 9], 136, 72, "swiglu"), ([1, 20], 2056, 64, "gelu"),      # tiles of few rows
+    ([700, 300], 264, 2600, "none"), ([700, 300], 264, 1336, "swiglu"),                           # pairs, gathered rows
+    ([2200, 1900], 2048, 5120, "none"),                                                           # put side by side first
+])
+def test_rows_outside_x_meet_infinities_in_w(counts, K, n, act):
+    """A row that an index outside x names is a row of zeros for every kernel: it gives zeros, and NaN in the columns where
+    its expert's w holds an infinity or NaN, as zeros do that lie in x. What row 0 of x holds does not matter."""
+    E, N, wide = len(counts), 50, 2 if act == "swiglu" else 1
+    d = S.Draw(K + n, "cuda")
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(off[-1])
+    idx = torch.from_numpy(np.random.default_rng(R).integers(1, N - 1, R).astype(np.int32))
+    at = [0, 1, R // 2, R - 1]
+    outside, inside = idx.clone(), idx.clone()
+    for i, v in zip(at, (-1, N, 1 << 30, -(1 << 31))):
+        outside[i], inside[i] = v, N - 1
+    x, w = d.normal((N, K)), d.normal((E, K, wide * n), 1 / math.sqrt(K))
+    x[0] = math.nan
+    x[N - 1] = 0
+    w[0, 5, 3], w[E - 1, K - 1, wide * n - 1] = math.inf, math.nan
+    ys = []
+    for rows in (outside, inside):
+        y = torch.full((R, n), MARK, device="cuda")
+        tp.tp_ragged_linear(x, N, dev(rows), dev(off), R, E, K, n, {"none": tp.TP_ACT_NONE, "gelu": tp.TP_ACT_GELU, "swiglu": tp.TP_ACT_SWIGLU}[act],
+                            w, y, tp.TP_F32)
+        settled()
+        ys.append(y)
+    assert torch.equal(ys[0].isnan(), ys[1].isnan()) and torch.equal(ys[0].nan_to_num(7), ys[1].nan_to_num(7))
+    for i in at:
+        e = 0 if i < off[1] else E - 1
+        z = torch.zeros(K, dtype=torch.float64, device="cuda") @ w[e].double()
+        want = z[:n] + z[n:] if act == "swiglu" else z
+        assert torch.equal(ys[0][i].isnan(), want.isnan()) and bool((ys[0][i].nan_to_num(0) == 0).all()), i
