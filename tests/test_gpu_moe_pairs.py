@@ -1,4 +1,4 @@
-"""What the CTA-pair kernels compute, against 64 bits."""
+"""What the CTA-pair kernels compute, and the whole MLP in every type, against 64 bits."""
 import math
 
 import numpy as np
@@ -7,7 +7,9 @@ import torch
 
 import synthetic as S
 import tensor_sharded_matmul_b200 as tp
-from test_gpu_moe import ACT, MARK, _lora_case, dev, settled
+from gpu_util import f64
+from oracle import moe as M
+from test_gpu_moe import ACT, DT, GATE, MARK, _lora_case, dev, rel, settled
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,44 @@ def test_lora_whose_first_product_takes_pairs(N, L, rank):
     """x A of so many adapters goes to the pair kernel, which applies each adapter's scale to its own rows."""
     ids = np.random.default_rng(N).integers(-1, L, N).astype(np.int32)
     _lora_case(N, 136, 6144, 8, L, rank, ids, N, scale=True)
+
+
+@pytest.mark.parametrize("types", ["f32 bf16 bf16", "bf16 f32 bf16", "bf16 bf16 f32", "f32 f32 f32"])
+@pytest.mark.parametrize("N,h,F,E,k,act,gate,masked", [
+    (37, 136, 72, 6, 2, "swiglu", "topk", 3), (300, 72, 200, 3, 2, "gelu", "softmax", 0),
+    (2100, 512, 2048, 4, 2, "swiglu", "topk", 11),           # pairs, rows put side by side, spans of weight gradients
+    (2100, 512, 2048, 4, 1, "gelu_tanh", "softmax", 1),
+])
+def test_mlp_in_every_type(N, h, F, E, k, act, gate, masked, types):
+    """Logits (and their gradient), y and dx in fp32 and bf16. z, u, du, dh and the rows of dx are rounded to bf16, each by at
+    most 2^-8 of the value; at most five of them lie on the way to an output, whose own rounding is a sixth: 2-norms of
+    the errors stay below 6 * 2^-8 of the output's."""
+    ld, yd, xd = (DT[v] for v in types.split())
+    d = S.Draw(N + F, "cuda")
+    wide, R = 2 if act == "swiglu" else 1, N * k
+    x, dy, logits = d.normal((N, h)), d.normal((N, h)), d.normal((N, E), 1.0, ld[1])
+    w_in, w_down = d.normal((E, h, wide * F), 1 / math.sqrt(h)), d.normal((E, F, h), 1 / math.sqrt(F))
+    logits[N - masked:] = -math.inf
+    new = lambda shape, dt=torch.bfloat16: torch.full(shape, math.nan, dtype=dt, device="cuda")           # noqa: E731
+    whole = lambda *shape: torch.full(shape, -9, dtype=torch.int32, device="cuda")                       # noqa: E731
+    expert, slot, offsets, row_token = whole(N, k), whole(N, k), whole(E + 1), whole(R)
+    weight, dweight, y, dx, dlogits = new((N, k), torch.float32), new((N, k), torch.float32), new((N, h), yd[1]), new((N, h), xd[1]), new((N, E), ld[1])
+    h_pre, z, u, du, dh = new((R, wide * F)), new((R, F)), new((R, h)), new((R, h)), new((R, wide * F))
+    dw_in, dw_down = new((E, h, wide * F), torch.float32), new((E, F, h), torch.float32)
+    nb = tp.tp_moe_mlp_ws_bytes(N, E, k)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    tp.tp_moe_mlp_fwd(x, N, h, F, E, k, GATE[gate], ACT[act], logits, ld[0], w_in, w_down, expert, weight, slot, offsets, row_token,
+                      h_pre, z, u, y, yd[0], ws, nb)
+    tp.tp_moe_mlp_bwd(x, dy, N, h, F, E, k, GATE[gate], ACT[act], logits, ld[0], w_in, w_down, expert, weight, slot, offsets,
+                      row_token, h_pre, z, u, du, dh, dweight, dw_in, dw_down, dx, xd[0], dlogits)
+    settled()
+    ref = M.moe_mlp_backward(f64(x), f64(logits), f64(w_in), f64(w_down), k, gate, act, f64(dy))
+    rows = len(ref["row_token"])
+    assert np.array_equal(expert.cpu().numpy(), ref["expert"]) and np.array_equal(offsets.cpu().numpy(), ref["offsets"])
+    assert np.array_equal(row_token[:rows].cpu().numpy(), ref["row_token"]) and np.array_equal(slot.cpu().numpy(), ref["slot"])
+    got = dict(y=y, dx=dx, dw_in=dw_in, dw_down=dw_down, dweight=dweight, z=z[:rows])
+    for name, v in got.items():
+        assert rel(v, ref[name]) < 6 * 2.0 ** -8, (name, rel(v, ref[name]))
+    if not (gate == "topk" and k == 1):
+        size = np.linalg.norm(M.gate_softmax(f64(logits), ref["expert"], gate) * np.abs(ref["dweight"]).max(initial=0))
+        assert np.linalg.norm(f64(dlogits) - ref["dlogits"]) < 6 * 2.0 ** -8 * size
