@@ -937,7 +937,7 @@ tp_status tp_moe_mlp_bwd(const uint16_t* x, const uint16_t* dy, int64_t N, int64
   if (tp_status st = tp_ragged_linear_dw(z, R, nullptr, du_ws, offsets, R, E, F, h, dw_down, TP_F32, stream)) return st;
   if (tp_status st = tp_ragged_linear_dx(du_ws, offsets, R, E, F, h, w_down, act, h_pre, dh_ws, stream)) return st;
   // du is not needed any more: where experts have many rows, x's gathered ones are put side by side there (8192 rows, 8
-  // experts, 4096 x 14336: 1120 us gathered, 850 side by side, 26 the copy; 384 rows an expert: 184 and 193)
+  // experts, 4096 x 14336: 970..1120 us gathered, 850 side by side, 26 the copy; 384 rows an expert: 184 and 193)
   const bool copy = R >= 512 * static_cast<int64_t>(E);
   if (copy) {
     if (tp_status st = gather_rows(x, N, row_token, offsets, E, R, h, du_ws, h, static_cast<cudaStream_t>(stream))) return st;

@@ -222,7 +222,11 @@ __device__ __forceinline__ void store_backward8(const RaggedParams& p, int64_t r
     unpack_bf8(h1, up);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-h[i]));   // within 2 ulp; 0 where expf overflows
+      // The sigmoid: __expf's argument is rounded, so that for negative h it is off by up to about (4 + 1.2 |h|) * 2^-23 of
+      // itself (2^-18 of itself at -24), for positive h by a few units; 0 where __expf overflows. The gradient's rounding to
+      // bf16 is 2^-9 on average; a division in place of the reciprocal would save 2 of those units (and took 159 us where
+      // this takes 137: 64 experts, 24558 rows, 1024 x 2048).
+      const float s = __fdividef(1.0f, 1.0f + __expf(-h[i]));
       dg[i] = f[i] * up[i] * (s * (1.0f + h[i] * (1.0f - s)));
       du[i] = f[i] * (h[i] * s);
     }

@@ -12,10 +12,10 @@
 // k-blocks, three stages fit.
 //
 // What bounds it: with rows side by side, the MMAs (their thread waits 90 cycles a stage, of 940); 8 experts of
-// 1024 rows, K = 4096, n = 14336, SwiGLU: 1330 us, 1450 TFLOP/s in a burst; under the power cap the clock falls to 1.2..1.6
-// GHz. Before the loading thread had a loop with little else than its loads, its 1500 cycles a stage were the bound
+// 1024 rows, K = 4096, n = 14336, SwiGLU: 1270..1330 us over the GPUs measured, 1450..1520 TFLOP/s in a burst of calls (with
+// `pre` written besides 1360 beside 1320); under the power cap the clock falls to 1.2..1.6 GHz. Before the loading thread had a loop with little else than its loads, its 1500 cycles a stage were the bound
 // (1600 us). (Stages of one k-block, six of them: 1480 us.)
-// Gathered rows (1820 us there): TMA's tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into
+// Gathered rows (1820 us there if all are fetched by index, 1430 put side by side first): TMA's tile::gather4 took about 75 cycles for four 128-byte rows, 221 TFLOP/s; loads into
 // registers two stages ahead, 897; cp.async by four warps, 922, by eight, 1089, by sixteen, 1076. What remains is the way
 // through a stage: 500 cycles to issue the copies, as many for them to land, and 1430 for the other CTA's release
 // at cluster scope to reach the leader, of 4100 for three stages. Wide products therefore put many gathered rows side
