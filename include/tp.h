@@ -342,8 +342,8 @@ tp_status tp_layer_fwd(const uint16_t* x, const uint16_t* const* o, int64_t N, i
  *     side by side at the end of y's own rows); no output may overlap an input or another output.
  *   - Kernels of these calls are launched to begin beside the kernel before them on the stream, and wait for it
  *     before they read or write anything: results are those of the stream's order. One exception, inside a call:
- *     tp_lora_linear's product of few tokens reads x, w, offsets and row_token while the call's own kernel for x . A
- *     runs, which itself has waited for all that came before the call.
+ *     tp_lora_linear's second product reads x, w, offsets and row_token while the call's own kernel for x . A
+ *     runs, which itself has waited for all that came before.
  * ------------------------------------------------------------------------------------------------ */
 #define TP_MAX_EXPERTS 1024
 #define TP_MAX_TOPK 16

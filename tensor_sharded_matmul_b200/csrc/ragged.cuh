@@ -52,8 +52,8 @@ struct RaggedParams {
 };
 
 // Launches a kernel that may begin while the one before it on the stream still runs: every thread of it waits
-// (wait_prerequisites) before it touches global memory, and then lets the next one begin. (One kernel reads some of its
-// inputs before its wait: ragged_kernel with adapters, see there.) Back to back
+// (wait_prerequisites) before it touches global memory, and then lets the next one begin. (The adapters' second product
+// reads some of its inputs before its wait: see ragged_kernel.) Back to back
 // such launches hide about 2 us each: the launch and, for the products, barriers and TMEM.
 template <typename... P, typename... A>
 tp_status launch_beside(const char* what, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A&&... args) {

@@ -226,10 +226,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
   }
-  wait_prerequisites();                              // up to here beside the kernel before, from here the next one beside this
+  // Up to here beside the kernel before, from here the next one beside this. Adapters: x, W and offsets are read without
+  // that wait, from L2, which the call's own kernel before this one has made safe (see ragged.cu); all else, the writes above
+  // all, comes behind it. (200 tokens, 4096 x 28672, rank 16: 70 us, waiting first 80; 4000 tokens, 4096 x 6144, rank 64: 274 and 279.)
+  if (!LORA) wait_prerequisites();
   launch_dependents();
   const int segs = LORA ? p.L : p.E;
-  for (int e = threadIdx.x; e <= segs; e += THREADS) s_off[e] = seg_bound(p.offsets, e, p.R);
+  for (int e = threadIdx.x; e <= segs; e += THREADS) {
+    if constexpr (LORA) s_off[e] = min(max(ld_gpu_s32(p.offsets + e), 0), p.R);
+    else s_off[e] = seg_bound(p.offsets, e, p.R);
+  }
   if (!LORA) {
     __syncthreads();
     if (warp == 2) count_units(p, s_off, s_first, lane);
@@ -272,9 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         runs = runs_of_half(p, row0, min(nh, t.i0 + t.valid - row0), lane, begin);
         x_both += 4096u * __popc(runs);
       }
-      const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
-      const int total_kb = num_kb + (chunks + 1) / 2;
       if (lane == 0) {
+        int chunks = LORA && u != pair ? ld_s32(tile_list(p, t)) * per_adapter : 0;
         auto load_kb = [&](int kb, uint32_t w, uint32_t x, uint32_t fb) {
           const int k0 = kb * BK;
           if (km) {
@@ -309,6 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ++loaded;
           if (++st == STAGES) { st = 0; phase ^= 1u; }
         }
+        if (LORA && u == pair) {                                      // the first tile's adapters, behind its x and W
+          wait_prerequisites();
+          chunks = ld_s32(tile_list(p, t)) * per_adapter;
+        }
+        const int total_kb = num_kb + (chunks + 1) / 2;
         int chunk = 0;
         for (; ok && kb < total_kb; kb += KB) {                       // a last odd k-block, and adapters
           ok = lane_wait(p, c, c.empty0 + 8 * st, phase ^ 1u, WAIT_PRODUCER_EMPTY);
@@ -357,11 +367,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int u = pair; ok; u += pairs) {
         const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
         if (!t.live) break;
-        const int chunks = LORA ? ld_s32(tile_list(p, t)) * per_adapter : 0;
-        const int total_kb = num_kb + (chunks + 1) / 2;
         const uint32_t idesc = idesc_bf16_f32(256, t.n_mma, !km, false);
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc) * 256u;
         if (lane == 0) {
+          int chunks = LORA && u != pair ? ld_s32(tile_list(p, t)) * per_adapter : 0;
           ok = lane_wait_cluster(p, c, c.acce0 + 8 * acc, acc_phase ^ 1u, WAIT_MMA_ACC_EMPTY);
           tc_fence_after();
           int kb = 0;
@@ -379,6 +388,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             umma_commit_pair_mc(c.empty0 + 8 * st, 0x3);
             if (++st == STAGES) { st = 0; phase ^= 1u; }
           }
+          if (LORA && u == pair) {                                    // as in warp 0
+            wait_prerequisites();
+            chunks = ld_s32(tile_list(p, t)) * per_adapter;
+          }
+          const int total_kb = num_kb + (chunks + 1) / 2;
           for (; ok && kb < total_kb; kb += KB) {                     // a last odd k-block, and adapters
             ok = lane_wait_cluster(p, c, c.full0 + 8 * st, phase, WAIT_MMA_FULL);
             if (!ok) break;
@@ -413,6 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     constexpr int ITEMS = CHUNK * GROUPS / 128;       // of a chunk, for each thread
     int acc = 0;
     uint32_t acc_phase = 0;
+    if (LORA) wait_prerequisites();
     for (int u = pair;; u += pairs) {
       const Tile t = find_tile<SWIGLU, LORA>(p, s_off, s_first, u, lane);
       if (!t.live) break;
@@ -521,6 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int piece = tid & 7, r0 = tid >> 3;
     const uint32_t line0 = smem_u32(c.sX) + r0 * 128 + ((piece ^ (r0 & 7)) << 4);   // (STEP is a multiple of 8)
     const int v_row = tid >> 1;                        // adapters: two threads build one row of 32 values
+    if (LORA) wait_prerequisites();
     int st = 0;
     uint32_t phase = 0, go_phase = 0;                  // go_phase: one bit per stage
     bool ok = true;
@@ -611,6 +627,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // phase's parity for the next one's. (The loaders cannot do it themselves: a release to the other CTA
     // waits for every copy that its thread has in flight.)
     const int mine = warp - RELAY0;
+    if (LORA) wait_prerequisites();
     int st = 0;
     uint32_t used_phase = 0;                           // one bit per stage
     bool ok = true;
