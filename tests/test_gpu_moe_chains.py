@@ -170,60 +170,61 @@ def test_mlp_over_shared_buffers(N, h, F, E):
             assert same(g[n], want[i][n]), (at, n)
 
 
-def test_captured_with_copies_and_a_fork():
+@pytest.mark.parametrize("N,n,t", [(100, 136, 1), (700, 5120, 2)])        # (700: the adapters' pairs)
+def test_captured_with_copies_and_a_fork(N, n, t):
     """A captured step whose calls follow copies, a cleared buffer and a join of two streams instead of kernels: its replays on
     new inputs are the eager calls'."""
-    N, h, F, E, L, rank = 100, 128, 96, 6, 4, 16
+    h, F, E, L, rank = 128, 96, 6, 4, 16
     runs = [_mlp(N, h, F, E, 2, "swiglu", "topk", seed=70 + i, masked=3) for i in range(2)]
     d = S.Draw(5, "cuda")
     source = [dict(x=d.normal((N, h)), logits=d.normal((N, E), 1.0, torch.float32), dy=d.normal((N, h)),
                    ids=torch.randint(-1, L, (N,), generator=d.gen, device="cuda", dtype=torch.int32)) for _ in range(3)]
-    feed = {n: v.clone() for n, v in source[0].items()}
-    w, a, b = d.normal((1, h, 136), 0.1), d.normal((L, h, rank), 0.1), d.normal((1, L, rank, 136), 0.5)
+    feed = {name: v.clone() for name, v in source[0].items()}
+    w, a, b = d.normal((t, h, n // t), 0.1), d.normal((L, h, rank), 0.1), d.normal((t, L, rank, n // t), 0.5)
     i32 = dict(dtype=torch.int32, device="cuda")
     ids, off, tok = torch.zeros(N, **i32), torch.zeros(L + 1, **i32), torch.zeros(N, **i32)
     pb, nb = tp.tp_lora_plan_ws_bytes(N, L), tp.tp_lora_ws_bytes(N, rank)
     pws, ws = torch.empty(pb, dtype=torch.uint8, device="cuda"), torch.empty(nb // 4, device="cuda")
-    out = torch.zeros((1, N, 136), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((t, N, n // t), dtype=torch.bfloat16, device="cuda")
     side = torch.cuda.Stream()
 
     def step():
         here = torch.cuda.current_stream()
         side.wait_stream(here)
         with torch.cuda.stream(side):                    # the other stream: its own copies, forward, backward
-            for n in ("x", "logits", "dy"):
-                runs[1][0][n].copy_(feed[n])
+            for name in ("x", "logits", "dy"):
+                runs[1][0][name].copy_(feed[name])
             runs[1][2](side), runs[1][3](side)
         ids.copy_(feed["ids"])
         tp.tp_lora_plan(ids, N, L, off, tok, pws, pb)    # directly behind a copy
         out.zero_()
-        tp.tp_lora_linear(feed["x"], N, h, 136, 1, w, L, rank, a, b, None, off, tok, out, ws, nb)
+        tp.tp_lora_linear(feed["x"], N, h, n, t, w, L, rank, a, b, None, off, tok, out, ws, nb)
         runs[0][0]["dy"].copy_(feed["dy"])
-        for n in ("x", "logits"):
-            runs[0][0][n].copy_(feed[n])
+        for name in ("x", "logits"):
+            runs[0][0][name].copy_(feed[name])
         runs[0][2](here)
         here.wait_stream(side)
         runs[0][3](here)                                 # directly behind the join
 
     def results():
         settled()
-        return [out.clone()] + [run[0][n].clone() for run in runs for n in OUT]
+        return [out.clone()] + [run[0][name].clone() for run in runs for name in OUT]
 
     want = []
     for src in source:
-        for n, v in src.items():
-            feed[n].copy_(v)
+        for name, v in src.items():
+            feed[name].copy_(v)
         step()
         want.append(results())
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         step()
     for i in (1, 0, 2, 1):
-        for n, v in source[i].items():
-            feed[n].copy_(v)
+        for name, v in source[i].items():
+            feed[name].copy_(v)
         for run in runs:
-            for n in KEPT:
-                run[0][n].fill_(NAN)
+            for name in KEPT:
+                run[0][name].fill_(NAN)
         ws.fill_(NAN)
         g.replay()
         for x, y in zip(results(), want[i]):
